@@ -1,6 +1,6 @@
 """Cases and plain forms of the serving-step operators: tables and slot maps of a step, the
-queries' and keys' norm and rotation with the cache write, and attention over a sliding window
-with a few first keys that stay visible.
+queries' and keys' norm and rotation with the cache write, attention over a sliding window with a
+few first keys that stay visible, and a decode step whose requests share a long prefix.
 
 ``run`` computes an operator in elementary torch operations (32-bit arithmetic, rounded once),
 or, where ``own`` is true, by the calls a user of the package makes. ``exact`` computes the same
@@ -23,9 +23,6 @@ def listed():
         # One decode step of a serving batch: 32 requests, one new token each (latency).
         dict(name="tables decode 32", op="tables", batch=32, min_rows=1, max_rows=1, min_hist=1024,
              max_hist=32768, page_size=16, lens=1),
-        # A continuous-batching step: chunks and single tokens of 256 requests.
-        dict(name="tables mixed 256", op="tables", batch=256, min_rows=0, max_rows=301, min_hist=0,
-             max_hist=5000, page_size=16, lens=2),
         # The largest step: over 100K new rows of 1,000 requests.
         dict(name="tables prefill 1000", op="tables", batch=1000, min_rows=1, max_rows=300,
              min_hist=0, max_hist=32768, page_size=64, lens=3),
@@ -37,10 +34,6 @@ def listed():
         dict(name="rope odd 1003", op="rope", rows=1003, pad=21, n_q_heads=32, n_kv_heads=8,
              head_dim=128, rot_dim=64, page_size=32, dtype="bf16", norm=True, interleaved=True,
              fused=True, max_pos=131072),
-        # The 2,048-row prefill chunk (24 query heads, 4 KV heads).
-        dict(name="rope chunk 2048", op="rope", rows=2048, pad=0, n_q_heads=24, n_kv_heads=4,
-             head_dim=256, rot_dim=128, page_size=64, dtype="bf16", norm=True, interleaved=False,
-             fused=False, max_pos=131072),
         # A whole 32,768-token prompt in one call.
         dict(name="rope prompt 32768", op="rope", rows=32768, pad=0, n_q_heads=16, n_kv_heads=2,
              head_dim=256, rot_dim=256, page_size=16, dtype="f16", norm=True, interleaved=False,
@@ -65,6 +58,12 @@ def listed():
         dict(name="window batch 6", op="prefill", batch=6, min_rows=1, max_rows=300, min_hist=0,
              max_hist=9000, window=1001, sinks=20, n_q_heads=32, n_kv_heads=8, head_dim=128,
              page_size=32, dtype="bf16", lens=8),
+        # 32 requests with one 32K-token prompt in common, each some hundred tokens past it.
+        dict(name="prefix decode 32", op="prefix", batch=32, pad=0, prefix=32768, max_own=1024,
+             n_q_heads=16, n_kv_heads=2, head_dim=256, page_size=16, dtype="f16", lens=9),
+        # A small padded batch on a short common prompt.
+        dict(name="prefix decode 7", op="prefix", batch=7, pad=2, prefix=2080, max_own=300,
+             n_q_heads=32, n_kv_heads=8, head_dim=128, page_size=32, dtype="bf16", lens=10),
     ]
 
 
@@ -79,7 +78,7 @@ HEADS = ((16, 2, 256), (24, 4, 256), (8, 1, 256), (32, 8, 128), (16, 2, 128), (8
 
 def draw(rng):
     """One more case of the listed ones' ranges."""
-    op = rng.choice(("tables", "rope", "decode", "prefill"))
+    op = rng.choice(("tables", "rope", "decode", "prefill", "prefix"))
     seed = rng.randrange(1 << 30)
     ps = rng.choice((16, 32, 64, 128))
     if op == "tables":
@@ -96,6 +95,11 @@ def draw(rng):
                     n_kv_heads=hkv, head_dim=d, rot_dim=16 * rng.randint(1, d // 16),
                     page_size=ps, dtype=dtype, norm=rng.random() < 0.75,
                     interleaved=rng.random() < 0.5, fused=rng.random() < 0.5, max_pos=131072)
+    if op == "prefix":
+        batch = _log_int(rng, 1, 64)
+        return dict(op=op, batch=batch, pad=rng.randint(0, batch // 4),
+                    prefix=ps * _log_int(rng, 1, 32768 // ps), max_own=_log_int(rng, 1, 1024),
+                    n_q_heads=hq, n_kv_heads=hkv, head_dim=d, page_size=ps, dtype=dtype, lens=seed)
     window, sinks = _log_int(rng, 1, 4096), rng.choice((0, 1, 4, 20, 128, 200))
     shape = dict(window=window, sinks=sinks, n_q_heads=hq, n_kv_heads=hkv, head_dim=d,
                  page_size=ps, dtype=dtype, lens=seed)
@@ -112,6 +116,9 @@ def draw(rng):
 def _lens(case):
     """(new rows, cached keys) of each sequence, by the case alone."""
     rng = random.Random(case["lens"])
+    if case["op"] == "prefix":  # the keys past the prefix count as new rows here
+        own_keys = [rng.randint(0, case["max_own"]) for _ in range(case["batch"])]
+        return own_keys, [case["prefix"]] * case["batch"]
     if case["op"] == "decode":
         lens = [rng.randint(case["min_len"], case["max_len"]) for _ in range(case["batch"])]
         lens[0] = max(lens[0], 1)
@@ -151,6 +158,12 @@ def work(case):
         heads = 2 * (hq + 2 * hkv) * d * 2  # each head's 16-bit row in and out
         angles = 4 * case["rot_dim"] * min(n, case["max_pos"])
         return {"bytes": n * (heads + 8) + angles, "flops": n * (hq + hkv) * d * 6}
+    if case["op"] == "prefix":  # the prefix is read once for all
+        lens = _lens(case)[0][case["pad"]:]
+        keys = case["prefix"] + sum(lens)
+        pairs = case["prefix"] * len(lens) + sum(lens)
+        return {"bytes": 2 * keys * hkv * d * 2 + 2 * case["batch"] * hq * d * 2,
+                "flops": 4 * d * hq * pairs}
     seen, pairs = _visible(case)
     keys = 0
     for sinks, lo, total in seen:
@@ -170,6 +183,8 @@ def prepare(case, seed):
         return _prepare_tables(case, gen)
     if case["op"] == "rope":
         return _prepare_rope(case, gen)
+    if case["op"] == "prefix":
+        return _prepare_prefix(case, gen)
     return _prepare_window(case, gen)
 
 
@@ -259,6 +274,33 @@ def _prepare_window(case, gen):
     return state
 
 
+def _prepare_prefix(case, gen):
+    own_keys, _ = _lens(case)
+    hq, hkv, d, ps = (case[x] for x in ("n_q_heads", "n_kv_heads", "head_dim", "page_size"))
+    dt, dev, batch, common = DTYPES[case["dtype"]], "cuda", case["batch"], case["prefix"] // ps
+    lens = [case["prefix"] + n if b >= case["pad"] else 0 for b, n in enumerate(own_keys)]
+    stride = max(1, -(-max(lens) // ps))
+    # every request's table row begins with the same pages; rows without a request hold none
+    page = torch.arange(stride, device=dev)[None, :]
+    seq = torch.tensor(lens, device=dev)[:, None]
+    table = torch.where((page < common) & (seq > 0), page, -1).to(torch.int32)
+    mine = (page >= common) & (page * ps < seq)
+    num_pages = common + int(mine.sum()) + 2
+    table[mine] = torch.arange(common, num_pages - 2, device=dev, dtype=torch.int32)
+    ids = torch.randperm(num_pages, generator=gen, device=dev).to(torch.int32)
+    table = torch.where(table >= 0, ids[table.long().clamp(min=0)], table)
+    pools = [torch.randn(num_pages, ps, hkv, d, generator=gen, device=dev).to(dt)
+             for _ in range(2)]
+    state = dict(case=case, q=torch.randn(batch, hq, d, generator=gen, device=dev).to(dt),
+                 k_pool=pools[0], v_pool=pools[1], table=table, prefix_table=ids[:common].clone(),
+                 seq_lens=_ints(lens), own_keys=max(lens) - case["prefix"] if any(lens) else 0)
+    if own:  # the plan of the step, which every layer of a model shares
+        from paged_kv_long_b200 import binding as pa
+        state["plan"] = pa.prefix_decode_plan(hq, hkv, d, ps, batch, case["prefix"],
+                                              max(1, max(lens)), dtype=case["dtype"])
+    return state
+
+
 # --------------------------------------------------------------------------------------- run
 
 
@@ -268,6 +310,8 @@ def run(s):
         return _own_tables(s) if own else _plain_tables(s)
     if op == "rope":
         return _own_rope(s) if own else _plain_rope(s)
+    if op == "prefix":
+        return _own_prefix(s) if own else _plain_prefix(s)
     return _own_window(s) if own else _plain_window(s)
 
 
@@ -294,6 +338,12 @@ def _own_window(s):
         return pa.window_decode(s["plan"], s["q"], s["k_pool"], s["v_pool"], s["table"],
                                 s["seq_lens"])
     return pa.window_prefill(s["plan"], s["q"], s["k_pool"], s["v_pool"], s["table"])
+
+
+def _own_prefix(s):
+    from paged_kv_long_b200 import binding as pa
+    return pa.prefix_decode(s["plan"], s["q"], s["k_pool"], s["v_pool"], s["prefix_table"],
+                            s["table"], s["seq_lens"])
 
 
 def _plain_tables(s):
@@ -386,6 +436,34 @@ def _plain_window(s):
     return out[live].to(s["q"].dtype)
 
 
+def _plain_prefix(s):
+    case = s["case"]
+    hq, hkv, d, ps = (case[x] for x in ("n_q_heads", "n_kv_heads", "head_dim", "page_size"))
+    b, g, common, dev = case["batch"], hq // hkv, case["prefix"], s["q"].device
+    seq = s["seq_lens"].long()[:, None]
+    q = s["q"].float().view(b, hkv, g, d)
+    # the common keys, once for all requests: [Hkv, prefix, D]
+    kc, vc = (p[s["prefix_table"].long()].flatten(0, 1).float().transpose(0, 1)
+              for p in (s["k_pool"], s["v_pool"]))
+    qc = q.transpose(0, 1).flatten(1, 2)  # [Hkv, B * G, D]
+    shared = (qc @ kc.transpose(1, 2)).view(hkv, b, g, common).transpose(0, 1)
+    # each request's own keys: [B, Hkv, keys, D]
+    key = common + torch.arange(s["own_keys"], device=dev)[None, :].expand(b, -1)
+    there = key < seq
+    page = s["table"].gather(1, (key // ps).clamp(max=s["table"].shape[1] - 1)).long()
+    slot = page.clamp(min=0) * ps + key % ps
+    ko, vo = (torch.where(there[:, :, None, None], p.flatten(0, 1)[slot], 0).float()
+              .transpose(1, 2) for p in (s["k_pool"], s["v_pool"]))
+    score = torch.cat([shared, q @ ko.transpose(2, 3)], dim=-1) * d ** -0.5
+    sees = torch.cat([(seq > 0).expand(b, common), there], dim=1)[:, None, None, :]
+    score = torch.where(sees, score, -torch.inf)
+    top = score.amax(-1, keepdim=True)
+    p = torch.exp(score - torch.where(top == -torch.inf, 0.0, top))
+    out = (p[..., :common].transpose(0, 1).flatten(1, 2) @ vc).view(hkv, b, g, d).transpose(0, 1)
+    out = (out + p[..., common:] @ vo) / p.sum(-1, keepdim=True).clamp(min=1e-30)
+    return out.flatten(1, 2).to(s["q"].dtype)
+
+
 # ------------------------------------------------------------------------------------- exact
 
 
@@ -393,6 +471,8 @@ def exact(case, seed):
     if case["op"] == "tables":  # whole numbers
         return None
     s = prepare(case, seed)
+    if case["op"] == "prefix":
+        return _exact_prefix(s)
     return _exact_rope(s) if case["op"] == "rope" else _exact_window(s)
 
 
@@ -447,4 +527,21 @@ def _exact_window(s):
             x = s["q"][row0:row0 + rows, h].double() @ k[:, h // (hq // hkv)].T / d ** 0.5
             weight = torch.softmax(x.masked_fill(hide, -torch.inf), dim=-1)
             out[row0:row0 + rows, h] = weight @ v[:, h // (hq // hkv)]
+    return out
+
+
+def _exact_prefix(s):
+    case = s["case"]
+    hkv, d, ps = (case[x] for x in ("n_kv_heads", "head_dim", "page_size"))
+    out = torch.zeros(s["q"].shape, dtype=torch.float64, device=s["q"].device)
+    for b, n in enumerate(s["seq_lens"].tolist()):
+        if not n:
+            continue
+        key = torch.arange(n, device=out.device)
+        slot = s["table"][b].long()[key // ps] * ps + key % ps
+        k, v = (p.view(-1, hkv, d)[slot].double() for p in (s["k_pool"], s["v_pool"]))
+        for h in range(hkv):
+            mine = slice(h * case["n_q_heads"] // hkv, (h + 1) * case["n_q_heads"] // hkv)
+            x = s["q"][b, mine].double() @ k[:, h].T / d ** 0.5
+            out[b, mine] = torch.softmax(x, dim=-1) @ v[:, h]
     return out
