@@ -66,7 +66,10 @@ typedef enum {
    * by pa_combine. Falls back to the makespan policy's uniform splits only when the
    * schedule would not fit the kernel's tables (512 items, 256 cut row blocks, 32 parts);
    * the plan's `policy` field says which was used. */
-  PA_POLICY_BALANCED = 3
+  PA_POLICY_BALANCED = 3,
+  /* Read only, in the plans of pa_window_plan and pa_window_decode_plan (pa_plan takes neither). */
+  PA_POLICY_WINDOW = 4,
+  PA_POLICY_WINDOW_DECODE = 5
 } pa_policy;
 
 /* Rows of the packed (token, head) Q tile, and keys per KV tile, of the kernel. */
@@ -278,6 +281,58 @@ int pa_batch_schedule_items(const pa_plan_t* plan, const int32_t* q_lens,
 int pa_batch_combine(const pa_plan_t* plan, const int32_t* q_lens, const int64_t* hist_lens,
                      const float* lse_ws, uint64_t ws_bytes, float* out, pa_stream_t stream);
 
+/*
+ * Sliding-window attention with sinks, on the same paged pools: the row at position p sees key
+ * j <= p when j > p - window (its last `window` keys, its own included) or j < n_sinks (the
+ * sequence's first keys, which stay visible). window >= 1, n_sinks >= 0; a window of the whole
+ * sequence is plain causal attention. Keys keep the positions that they were rotated with.
+ *   Pages that lie wholly between the sinks and the window of every row of the call may have been
+ * given back: their table entries are never used and may hold anything (-1, another sequence's
+ * page). Any other slot that no row of the launch sees may hold any bits, NaN included. A
+ * non-finite key or value that some row does see may reach other rows of the same sequence (rows
+ * share key tiles).
+ *   out has the type of q: the sums are fp32, split partials too, and the row is rounded once.
+ * Softmax and products are those of pa_prefill (probabilities rounded to the input type).
+ * The pages have no counterpart; it is the attention of models whose local layers see a window,
+ * and of caches bounded to a window and the first tokens.
+ *
+ * pa_window_plan / pa_window_prefill — several sequences in one launch, each a chunk of q_lens[b]
+ * rows after hist_lens[b] keys: arguments, limits and layouts of pa_batch_plan and
+ * pa_batch_prefill, with the window, the sinks and the output's type. pa_window_prefill also
+ * merges the parts of cut row blocks (there is no separate combine). A single piece is a batch of
+ * one, a decode step with host lengths a batch of one-row chunks. The plan's policy is
+ * PA_POLICY_WINDOW, and `window`, `n_sinks` and the arrays must be those it was made with; other
+ * entry points refuse the plan. pa_window_schedule_items lists its items: kt0 and kt1 count along
+ * the row block's visible KV tiles (the sinks' tiles, then the window's).
+ */
+int pa_window_plan(int num_sms, int n_q_heads, int n_kv_heads, int head_dim, int page_size,
+                   int batch, const int32_t* q_lens, const int64_t* hist_lens, int window,
+                   int n_sinks, int dtype, float scale, pa_plan_t* plan);
+int pa_window_prefill(const pa_plan_t* plan, const int32_t* q_lens, const int64_t* hist_lens,
+                      int window, int n_sinks, const void* q, const void* k_pool,
+                      const void* v_pool, const int32_t* block_table, int table_stride,
+                      int64_t num_pages, void* out, float* lse_ws, uint64_t ws_bytes,
+                      pa_stream_t stream);
+int pa_window_schedule_items(const pa_plan_t* plan, const int32_t* q_lens,
+                             const int64_t* hist_lens, int window, int n_sinks, int32_t* items,
+                             int cap);
+
+/*
+ * pa_window_decode_plan / pa_window_decode — one query token per sequence, lengths on the device:
+ * arguments, limits and layouts of pa_decode_plan and pa_decode, with the window, the sinks and
+ * the output's type; the S splits share a sequence's visible KV tiles. pa_window_decode also
+ * merges the splits. A sequence with no key (a padded row) gets zeros. The plan's policy is
+ * PA_POLICY_WINDOW_DECODE and its hist_len max_seq_len; `window` and `n_sinks` must be those it
+ * was made with (a larger window gives right results too, in longer units).
+ */
+int pa_window_decode_plan(int num_sms, int n_q_heads, int n_kv_heads, int head_dim, int page_size,
+                          int batch, int64_t max_seq_len, int window, int n_sinks, int dtype,
+                          float scale, int splits_override, pa_plan_t* plan);
+int pa_window_decode(const pa_plan_t* plan, int window, int n_sinks, const void* q,
+                     const void* k_pool, const void* v_pool, const int32_t* block_table,
+                     int table_stride, const int32_t* seq_lens, int64_t num_pages, void* out,
+                     float* lse_ws, uint64_t ws_bytes, pa_stream_t stream);
+
 /* Bytes of the device-resident scratch used by pa_prefill_noalloc (64 MiB). */
 #define PA_NOALLOC_WS_BYTES (64ull << 20)
 
@@ -335,6 +390,71 @@ int pa_kv_append(int n_kv_heads, int head_dim, int page_size, int dtype, const v
 int pa_kv_publish(int n_kv_heads, int head_dim, int page_size, int dtype, const void* k_staged,
                   const void* v_staged, void* k_pool, void* v_pool, const int32_t* page_table,
                   int64_t num_pages, int64_t first_pos, int rows, pa_stream_t stream);
+
+/* Requests of one pa_block_tables call. */
+#define PA_STEP_MAX_SEQS 4096
+
+/*
+ * pa_block_tables — the bookkeeping of a serving step on the device, from the requests' lengths
+ * alone (no host copy; the step before pa_qk_rope_append): pages for the new rows, the block
+ * table's new entries, and every new row's position and pool slot. One kernel on `stream`.
+ *   q_lens, hist_lens  device int32 [batch]: new rows and cached keys of each request, >= 0.
+ *   free_pages         device int32 [n_free]: pages in no table row; taken in order.
+ *   pages_used         device int32 [1]: entries of free_pages that earlier steps took;
+ *   pages_used_out     device int32 [1], not the same word: that plus the pages taken here.
+ *   block_table        device int32 [batch][table_stride], updated in place: request b owns
+ *                      entries 0 .. ceil(h/PS)-1 (only read) and gets the entries up to
+ *                      ceil((h+r)/PS)-1 from the free list, request by request. Others stay.
+ *   slots, positions   device int32 [max_rows]: row R_b + i of the packed step (R_b = rows of the
+ *                      requests before b) has position h_b + i and pool slot page * PS + offset;
+ *                      rows behind the last request get -1 in both, so a captured graph with
+ *                      max_rows above the step's rows writes nothing for them.
+ *   cu_q_lens          device int32 [batch + 1]: the R_b, then the step's rows.
+ *   seq_lens           device int32 [batch]: h + r (pa_decode's lengths).
+ * Raises PA_ERR_PAGE_INDEX in pa_device_error, and goes on: for a negative length (read as 0), for
+ * more rows than max_rows (the first max_rows are mapped), for a row past its table row, the end
+ * of the free list or a page outside [0, num_pages) (slot -1; a table entry taken from past the
+ * list's end is -1). Returns PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED (page_size not a power
+ * of two in 16..128, batch > PA_STEP_MAX_SEQS, pools of 2^31 slots) or PA_ERR_CUDA.
+ */
+int pa_block_tables(int batch, const int32_t* q_lens, const int32_t* hist_lens, int page_size,
+                    int64_t num_pages, const int32_t* free_pages, int n_free,
+                    const int32_t* pages_used, int32_t* pages_used_out, int32_t* block_table,
+                    int table_stride, int max_rows, int32_t* slots, int32_t* positions,
+                    int32_t* cu_q_lens, int32_t* seq_lens, pa_stream_t stream);
+
+/*
+ * pa_qk_rope_append — from the projections to attention in one pass over a step's packed rows:
+ * the norm of each query and key head, the rotation by position, and the write of the keys and
+ * values into their pool slots (pa_kv_append for rows of any sequences).
+ *   q, k, v        device, of dtype: row t at q + t * q_stride elements, [Hq][D] contiguous (k, v:
+ *                  [Hkv][D]); strides are multiples of 8, so the three may be views of the rows
+ *                  of one fused projection. Pointers 16-byte aligned.
+ *   q_weight, k_weight  device, D values of dtype (weight_f32 = 0) or fp32 (1), 16-byte aligned:
+ *                  y = x / sqrt(mean(x^2) + eps) * w over each head. NULL: that side has no norm.
+ *   rope           device fp32 [max_pos][rot_dim]: row p holds rot_dim/2 cosines, then as many
+ *                  sines, of position p's angles. rot_dim: a multiple of 16 up to D; the values
+ *                  past it are not rotated. Pairs are (i, i + rot_dim/2), or (2i, 2i+1) when
+ *                  interleaved: (a, b) -> (a cos - b sin, b cos + a sin).
+ *   positions      device int32 [rows]; slots device int32 [rows] (see pa_block_tables). A row
+ *                  with a negative slot is skipped: nothing of it is written, q_out included. A
+ *                  slot past the pool or a position outside [0, max_pos) skips the row too and
+ *                  raises PA_ERR_PAGE_INDEX in pa_device_error. Slots of a call must differ:
+ *                  rows of the same slot would leave a mixture of their heads there.
+ *   q_out          device [rows][Hq][D] of dtype, contiguous; q itself (q_stride = Hq*D) or memory
+ *                  that overlaps no input.
+ *   k_pool, v_pool device [num_pages][PS][Hkv][D] of dtype; only the rows' slots change.
+ * All arithmetic is fp32 (sums of squares too), rounded once to dtype.
+ * Returns PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED (head_dim not 64/128/256, rot_dim,
+ * page_size, pools of 2^31 slots) or PA_ERR_CUDA.
+ */
+int pa_qk_rope_append(int n_q_heads, int n_kv_heads, int head_dim, int page_size, int dtype,
+                      int rows, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                      const void* v, int64_t v_stride, const int32_t* positions,
+                      const int32_t* slots, const float* rope, int rot_dim, int64_t max_pos,
+                      int interleaved, const void* q_weight, const void* k_weight, int weight_f32,
+                      float eps, void* q_out, void* k_pool, void* v_pool, int64_t num_pages,
+                      pa_stream_t stream);
 
 /*
  * pa_device_error — synchronise the current device, then read (and with reset != 0,

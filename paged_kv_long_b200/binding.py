@@ -7,6 +7,7 @@ no CPU fallback: if the library is missing or a tensor is not on a CUDA device, 
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import math
 import os
@@ -24,7 +25,9 @@ EXPORTED = ("pa_plan", "pa_prefill", "pa_combine", "pa_prefill_noalloc", "pa_dev
             "pa_selftest_timeout", "pa_status_string", "pa_cores_policy_splits",
             "pa_legacy_policy_splits", "pa_schedule_items", "pa_kv_append", "pa_pieces",
             "pa_decode_plan", "pa_decode", "pa_batch_plan", "pa_batch_prefill",
-            "pa_batch_combine", "pa_batch_schedule_items", "pa_kv_publish")
+            "pa_batch_combine", "pa_batch_schedule_items", "pa_kv_publish",
+            "pa_window_plan", "pa_window_prefill", "pa_window_schedule_items",
+            "pa_window_decode_plan", "pa_window_decode", "pa_block_tables", "pa_qk_rope_append")
 
 
 class PaError(RuntimeError):
@@ -111,6 +114,28 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.pa_batch_schedule_items.restype = i32
     lib.pa_kv_publish.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, i64, i64, i32, vp]
     lib.pa_kv_publish.restype = i32
+    lib.pa_window_plan.argtypes = [i32, i32, i32, i32, i32, i32, vp, vp, i32, i32, i32,
+                                   ctypes.c_float, ctypes.POINTER(Plan)]
+    lib.pa_window_plan.restype = i32
+    lib.pa_window_prefill.argtypes = [ctypes.POINTER(Plan), vp, vp, i32, i32, vp, vp, vp, vp, i32,
+                                      i64, vp, vp, u64, vp]
+    lib.pa_window_prefill.restype = i32
+    lib.pa_window_schedule_items.argtypes = [ctypes.POINTER(Plan), vp, vp, i32, i32,
+                                             ctypes.POINTER(ctypes.c_int32), i32]
+    lib.pa_window_schedule_items.restype = i32
+    lib.pa_window_decode_plan.argtypes = [i32, i32, i32, i32, i32, i32, i64, i32, i32, i32,
+                                          ctypes.c_float, i32, ctypes.POINTER(Plan)]
+    lib.pa_window_decode_plan.restype = i32
+    lib.pa_window_decode.argtypes = [ctypes.POINTER(Plan), i32, i32, vp, vp, vp, vp, i32, vp, i64,
+                                     vp, vp, u64, vp]
+    lib.pa_window_decode.restype = i32
+    lib.pa_block_tables.argtypes = [i32, vp, vp, i32, i64, vp, i32, vp, vp, vp, i32, i32, vp, vp,
+                                    vp, vp, vp]
+    lib.pa_block_tables.restype = i32
+    lib.pa_qk_rope_append.argtypes = [i32, i32, i32, i32, i32, i32, vp, i64, vp, i64, vp, i64, vp,
+                                      vp, vp, i32, i64, i32, vp, vp, i32, ctypes.c_float, vp, vp,
+                                      vp, i64, vp]
+    lib.pa_qk_rope_append.restype = i32
     if path is None:
         _lib = lib
     return lib
@@ -468,6 +493,303 @@ def batch_prefill(bp: BatchPlan, q, k_pool, v_pool, block_table, out=None, ws=No
     _check(lib.pa_batch_combine(ctypes.byref(p), ql, hl, ws_ptr, ws_bytes, out.data_ptr(),
                                 _stream_ptr(stream)), "pa_batch_combine")
     return out
+
+
+class WindowPlan:
+    """A plan with its window and sinks (pa_window_plan with the host length arrays it was made
+    from, or pa_window_decode_plan without)."""
+
+    def __init__(self, plan: Plan, window: int, n_sinks: int, q_lens=None, hist_lens=None):
+        self.plan = plan
+        self.window = window
+        self.n_sinks = n_sinks
+        self.q_lens = q_lens
+        self.hist_lens = hist_lens
+
+
+def _num_sms() -> int:
+    import torch
+    return torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+
+
+def _window_args(window, n_sinks):
+    """window and n_sinks as the 32-bit C arguments (a larger window sees every key anyway)."""
+    window, n_sinks = int(window), int(n_sinks)
+    if window < 1 or n_sinks < 0:
+        raise ValueError("window must be >= 1 and n_sinks >= 0")
+    return min(window, 2**31 - 1), min(n_sinks, 2**31 - 1)
+
+
+def window_plan(n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, q_lens, hist_lens,
+                window: int, n_sinks: int = 0, dtype="bf16", scale: float = 0.0,
+                num_sms: int | None = None) -> WindowPlan:
+    """pa_window_plan: the schedule of a batch of chunks under a sliding window with sinks (host
+    only; one sequence is a batch of one)."""
+    import numpy as np
+    window, n_sinks = _window_args(window, n_sinks)
+    q_lens = np.ascontiguousarray(q_lens, dtype=np.int32)
+    hist_lens = np.ascontiguousarray(hist_lens, dtype=np.int64)
+    if q_lens.shape != hist_lens.shape or q_lens.ndim != 1:
+        raise ValueError("q_lens and hist_lens must be 1-D of the same length")
+    p = Plan()
+    st = load_library().pa_window_plan(num_sms or _num_sms(), n_q_heads, n_kv_heads, head_dim,
+                                       page_size, len(q_lens), q_lens.ctypes.data,
+                                       hist_lens.ctypes.data, window, n_sinks,
+                                       _dtype_code(dtype), scale, ctypes.byref(p))
+    _check(st, "pa_window_plan")
+    return WindowPlan(p, window, n_sinks, q_lens, hist_lens)
+
+
+def window_schedule_items(wp: WindowPlan):
+    """pa_window_schedule_items: int32 [n, 4] of (global row block, kt0, kt1, slot or -1), kt0 and
+    kt1 along the row block's visible KV tiles."""
+    import numpy as np
+    if wp.q_lens is None:
+        raise ValueError("a decode plan has no items")
+    args = (ctypes.byref(wp.plan), wp.q_lens.ctypes.data, wp.hist_lens.ctypes.data, wp.window,
+            wp.n_sinks)
+    n = load_library().pa_window_schedule_items(*args, None, 0)
+    if n < 0:
+        raise PaError(n, "pa_window_schedule_items")
+    out = np.zeros((max(n, 1), 4), dtype=np.int32)
+    load_library().pa_window_schedule_items(
+        *args, out.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), n)
+    return out[:n]
+
+
+def window_decode_plan(n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, batch: int,
+                       max_seq_len: int, window: int, n_sinks: int = 0, dtype="bf16",
+                       scale: float = 0.0, splits: int = 0,
+                       num_sms: int | None = None) -> WindowPlan:
+    """pa_window_decode_plan: split count and workspace of a decode step under a sliding window
+    with sinks (host only)."""
+    window, n_sinks = _window_args(window, n_sinks)
+    p = Plan()
+    st = load_library().pa_window_decode_plan(num_sms or _num_sms(), n_q_heads, n_kv_heads,
+                                              head_dim, page_size, batch, max_seq_len, window,
+                                              n_sinks, _dtype_code(dtype), scale, splits,
+                                              ctypes.byref(p))
+    _check(st, "pa_window_decode_plan")
+    return WindowPlan(p, window, n_sinks)
+
+
+def _same_device(first, *rest):
+    """All tensors (None skipped) sit on one CUDA device; returns it."""
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}: one device is needed")
+    return first.device
+
+
+def _call(device, stream, fn, name, *args):
+    """fn(*args, stream) with `device` current, on its current stream unless one is given."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, _stream_ptr(stream))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream_ptr(stream))
+    _check(st, name)
+
+
+def _used_on(stream, *tensors):
+    """Tensors made here (on the current stream) that the call uses on `stream`: their memory is
+    not handed out again before that work is done."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def _window_tensors(p: Plan, rows, q, k_pool, v_pool, block_table, out, ws, stream):
+    """Checks of the tensors that both window calls take; (out, ws, ws pointer, ws bytes)."""
+    import torch
+    dt = _torch_dtype(p)
+    Hq, Hkv, D, PS = p.n_q_heads, p.n_kv_heads, p.head_dim, p.page_size
+    _require_cuda(q, "q", dt, (rows, Hq, D))
+    _require_cuda(k_pool, "k_pool", dt)
+    _require_cuda(v_pool, "v_pool", dt, k_pool.shape)
+    if k_pool.dim() != 4 or k_pool.shape[1:] != (PS, Hkv, D):
+        raise ValueError("k_pool must be [num_pages, page_size, Hkv, D]")
+    _require_cuda(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2 or block_table.shape[0] != p.batch:
+        raise ValueError("block_table must be [batch, max_pages]")
+    if out is None:
+        out = torch.empty_like(q)
+        _used_on(stream, out)
+    else:
+        _require_cuda(out, "out", dt, (rows, Hq, D))
+    ws_ptr, ws_bytes = None, 0
+    if p.ws_bytes > 0:
+        if ws is None:
+            ws = workspace(p, q.device)
+            _used_on(stream, ws)
+        else:
+            _require_cuda(ws, "ws", torch.float32)
+        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel() * 4
+    _same_device(q, k_pool, v_pool, block_table, out, ws)
+    return out, ws, ws_ptr, ws_bytes
+
+
+def window_decode(wp: WindowPlan, q, k_pool, v_pool, block_table, seq_lens, out=None, ws=None,
+                  stream=None):
+    """pa_window_decode: one query token per sequence against the last `window` keys and the first
+    `n_sinks` of that sequence (see include/pa.h). q [B, Hq, D]; block_table int32
+    [B, max_pages]; seq_lens int32 [B]. Returns out [B, Hq, D] of q's type."""
+    import torch
+    p = wp.plan
+    if wp.q_lens is not None:
+        raise ValueError("a plan of window_plan runs with window_prefill")
+    _require_cuda(seq_lens, "seq_lens", torch.int32, (p.batch,))
+    out, ws, ws_ptr, ws_bytes = _window_tensors(p, p.batch, q, k_pool, v_pool, block_table, out,
+                                                ws, stream)
+    _call(_same_device(q, seq_lens), stream, load_library().pa_window_decode, "pa_window_decode",
+          ctypes.byref(p), wp.window, wp.n_sinks, q.data_ptr(), k_pool.data_ptr(),
+          v_pool.data_ptr(), block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(),
+          k_pool.shape[0], out.data_ptr(), ws_ptr, ws_bytes)
+    return out
+
+
+def window_prefill(wp: WindowPlan, q, k_pool, v_pool, block_table, out=None, ws=None, stream=None):
+    """pa_window_prefill: the chunks of a batch under the plan's sliding window and sinks (see
+    include/pa.h). q [sum q_lens, Hq, D] packed in order; block_table int32 [batch, max_pages].
+    Returns out [sum q_lens, Hq, D] of q's type."""
+    p = wp.plan
+    if wp.q_lens is None:
+        raise ValueError("a plan of window_decode_plan runs with window_decode")
+    out, ws, ws_ptr, ws_bytes = _window_tensors(p, p.chunk_rows, q, k_pool, v_pool, block_table,
+                                                out, ws, stream)
+    _call(q.device, stream, load_library().pa_window_prefill, "pa_window_prefill",
+          ctypes.byref(p), wp.q_lens.ctypes.data, wp.hist_lens.ctypes.data, wp.window, wp.n_sinks,
+          q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(),
+          block_table.shape[1], k_pool.shape[0], out.data_ptr(), ws_ptr, ws_bytes)
+    return out
+
+
+StepTables = collections.namedtuple("StepTables",
+                                    "slots positions cu_q_lens seq_lens pages_used")
+
+
+def block_tables(q_lens, hist_lens, free_pages, pages_used, block_table, max_rows: int,
+                 page_size: int, num_pages: int, out: StepTables | None = None,
+                 stream=None) -> StepTables:
+    """pa_block_tables: the step's pages taken from the free list into block_table (in place),
+    and every new row's pool slot and position (see include/pa.h). q_lens, hist_lens int32 [B];
+    free_pages int32 [F]; pages_used int32 [1]; block_table int32 [B, max_pages]. Returns
+    StepTables(slots [max_rows], positions [max_rows], cu_q_lens [B + 1], seq_lens [B],
+    pages_used [1]), in the tensors of `out` when given (its pages_used not the input's)."""
+    import torch
+    i32 = torch.int32
+    _require_cuda(q_lens, "q_lens", i32)
+    if q_lens.dim() != 1:
+        raise ValueError("q_lens must be [batch]")
+    B = q_lens.shape[0]
+    _require_cuda(hist_lens, "hist_lens", i32, (B,))
+    _require_cuda(free_pages, "free_pages", i32)
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must be 1-D")
+    _require_cuda(pages_used, "pages_used", i32, (1,))
+    _require_cuda(block_table, "block_table", i32)
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [batch, max_pages]")
+    sizes = (max_rows, max_rows, B + 1, B, 1)
+    if out is None:  # one allocation, cut at multiples of four words
+        starts, total = [], 0
+        for n in sizes:
+            starts.append(total)
+            total += (n + 3) & ~3
+        buf = torch.empty(total, dtype=i32, device=q_lens.device)
+        _used_on(stream, buf)
+        out = StepTables(*(buf[a:a + n] for a, n in zip(starts, sizes)))
+    else:
+        out = StepTables(*out)
+        for t, name, n in zip(out, StepTables._fields, sizes):
+            _require_cuda(t, name, i32, (n,))
+    device = _same_device(q_lens, hist_lens, free_pages, pages_used, block_table, *out)
+    _call(device, stream, load_library().pa_block_tables, "pa_block_tables", B, q_lens.data_ptr(),
+          hist_lens.data_ptr(), page_size, num_pages, free_pages.data_ptr(), free_pages.shape[0],
+          pages_used.data_ptr(), out.pages_used.data_ptr(), block_table.data_ptr(),
+          block_table.shape[1], max_rows, out.slots.data_ptr(), out.positions.data_ptr(),
+          out.cu_q_lens.data_ptr(), out.seq_lens.data_ptr())
+    return out
+
+
+def rope_table(max_pos: int, rot_dim: int, theta: float = 10000.0, device="cuda"):
+    """The rotation table that qk_rope_append reads: fp32 [max_pos, rot_dim], row p the cosines
+    and then the sines of p * theta^(-2i / rot_dim), i < rot_dim / 2, from angles in 64 bits."""
+    import torch
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device)
+    angle = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] \
+        * float(theta) ** (-i / rot_dim)
+    return torch.cat([angle.cos(), angle.sin()], dim=1).float()
+
+
+def _require_rows(t, name, dtype, shape):
+    """t is [rows, H, D] on CUDA with contiguous rows; returns its row stride in elements."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    width = shape[1] * shape[2]
+    s0, s1, s2 = t.stride()
+    if (s1 != shape[2] and shape[1] > 1) or s2 != 1:
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    if shape[0] <= 1:
+        return width
+    if s0 < width or s0 % 8:
+        raise ValueError(f"the row stride of {name} must be a multiple of 8 and cover the row")
+    return s0
+
+
+def qk_rope_append(q, k, v, positions, slots, rope, k_pool, v_pool, q_weight=None, k_weight=None,
+                   eps: float = 1e-6, interleaved: bool = False, q_out=None, stream=None):
+    """pa_qk_rope_append: norm (where a weight is given) and rotation of each query and key head,
+    the keys and values written into their pool slots (see include/pa.h). q [T, Hq, D], k and v
+    [T, Hkv, D], rows of any stride; positions and slots int32 [T] (a negative slot skips the
+    row); rope fp32 [max_pos, rot_dim] (rope_table); pools [num_pages, PS, Hkv, D]. Returns
+    q_out [T, Hq, D] (q itself may be given, when contiguous)."""
+    import torch
+    if not isinstance(q, torch.Tensor) or q.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("q must be a float16 or bfloat16 tensor")
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, Hq, D]")
+    dt = q.dtype
+    T, Hq, D = q.shape
+    _require_cuda(k_pool, "k_pool", dt)
+    if k_pool.dim() != 4 or k_pool.shape[3] != D:
+        raise ValueError("k_pool must be [num_pages, page_size, Hkv, D]")
+    num_pages, PS, Hkv, _ = k_pool.shape
+    _require_cuda(v_pool, "v_pool", dt, k_pool.shape)
+    q_stride = _require_rows(q, "q", dt, (T, Hq, D))
+    k_stride = _require_rows(k, "k", dt, (T, Hkv, D))
+    v_stride = _require_rows(v, "v", dt, (T, Hkv, D))
+    _require_cuda(positions, "positions", torch.int32, (T,))
+    _require_cuda(slots, "slots", torch.int32, (T,))
+    _require_cuda(rope, "rope", torch.float32)
+    if rope.dim() != 2:
+        raise ValueError("rope must be [max_pos, rot_dim]")
+    weights = [w for w in (q_weight, k_weight) if w is not None]
+    for w in weights:
+        _require_cuda(w, "q_weight and k_weight", None, (D,))
+        if w.dtype != weights[0].dtype or w.dtype not in (dt, torch.float32):
+            raise TypeError(f"q_weight and k_weight must both be {dt} or both float32")
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+        _used_on(stream, q_out)
+    else:
+        _require_cuda(q_out, "q_out", dt, (T, Hq, D))
+    device = _same_device(q, k, v, positions, slots, rope, k_pool, v_pool, q_out, *weights)
+    _call(device, stream, load_library().pa_qk_rope_append, "pa_qk_rope_append", Hq, Hkv, D, PS,
+          _dtype_code(dt), T, q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(),
+          v_stride, positions.data_ptr(), slots.data_ptr(), rope.data_ptr(), rope.shape[1],
+          rope.shape[0], 1 if interleaved else 0,
+          None if q_weight is None else q_weight.data_ptr(),
+          None if k_weight is None else k_weight.data_ptr(),
+          1 if weights and weights[0].dtype == torch.float32 else 0, eps, q_out.data_ptr(),
+          k_pool.data_ptr(), v_pool.data_ptr(), num_pages)
+    return q_out
 
 
 def device_error(reset: bool = True) -> tuple[int, int]:

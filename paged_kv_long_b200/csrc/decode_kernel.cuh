@@ -73,7 +73,8 @@ __device__ __forceinline__ uint16_t to16(float x) {
 // key range; an uncut row block writes the output, a part of a cut one its partial and LSE in
 // the item's workspace slot, merged by combine_blocks_kernel). Otherwise block b is decode unit
 // b of pa_decode (device lengths, uniform splits).
-template <int D, bool BF16, bool BAL>
+// WIN: sliding window with sinks, 16-bit output.
+template <int D, bool BF16, bool BAL, bool WIN>
 __device__ __forceinline__ void decode_body(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                             const PrefillArgs& a_in, const ItemTable* items) {
   PrefillArgs a = a_in;
@@ -89,26 +90,27 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& tm_k, const CUten
   int64_t kt0, kt1;
   if constexpr (BAL) {
     const PaItem it = items->item[blockIdx.x];
-    const int32_t rb = batch_rebase<D>(a, *items, it.rb);  // one Q tile per sequence: g = rb
+    const int32_t rb = batch_rebase<D, WIN>(a, *items, it.rb);  // one Q tile per sequence: g = rb
     int64_t qt;
     rb_coords(rb, a.q_tiles, a.Hkv, &qt, &g);
     kt0 = it.kt0;
     kt1 = it.kt1;
     slot = it.slot;
+    if constexpr (WIN) set_window(a, a.hist_len, a.hist_len);
   } else {
-    decode_unit<D>(a, reinterpret_cast<int32_t*>(smem + C::RING_OFF), &g, &s, &kt0, &kt1);
+    decode_unit<D, WIN>(a, reinterpret_cast<int32_t*>(smem + C::RING_OFF), &g, &s, &kt0, &kt1);
   }
   const int n = (int)(kt1 - kt0);
   if (n == 0) {
-    empty_unit<D>(a, 0, g, s);
+    empty_unit<D, WIN>(a, 0, g, s);
     return;
   }
 
   int32_t pre_row0 = a.oob_row, pre_row1 = a.oob_row;
   if (warp > kMmaWarp) {
     const bool report = warp == kMmaWarp + 1;
-    pre_row0 = tile_page_row<true>(a, kt0, n, 0, lane, report);
-    pre_row1 = tile_page_row<true>(a, kt0, n, 1, lane, report);
+    pre_row0 = tile_page_row<true, WIN>(a, kt0, n, 0, lane, report);
+    pre_row1 = tile_page_row<true, WIN>(a, kt0, n, 1, lane, report);
   }
   auto bar = [&](int i) -> uint32_t { return sb + C::BAR_OFF + 8u * (uint32_t)i; };
   auto slot_addr = [&](uint32_t r) -> uint32_t { return sb + C::RING_OFF + r * kPanel; };
@@ -182,8 +184,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& tm_k, const CUten
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const int sbuf = j & 1;
-      const int64_t key0 = (kt0 + j) * kTileKeys;
-      const bool live = key0 + t < a.total_keys;
+      const int64_t key0 = kv_tile<WIN>(a, kt0 + j) * kTileKeys;
+      const bool live = !key_unseen<WIN>(a, key0 + t);
       float sv[8];
       if (ok) ok = warp_wait(bar(C::B_SFULL + sbuf), (j >> 1) & 1, abort_flag, tmo);
       if (ok) {
@@ -254,12 +256,17 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& tm_k, const CUten
       // completes phase i/2 of pv_done[i % 2]; as in the prefill kernels no phase is skipped.
       if (ok && j >= 2)
         ok = warp_wait(bar(C::B_PVDONE + sbuf), ((j - 2) >> 1) & 1, abort_flag, tmo);
-      if (ok && key0 + kTileKeys > a.total_keys) {
+      if (ok && tile_unseen<WIN>(a, key0)) {
         // The tail tile: V rows of keys past the sequence (in its last page) hold arbitrary
         // bits and P is 0 there, but 0 * NaN is NaN inside the MMA, so those rows are zeroed.
         // Once PV(j-1) is done, every earlier fill of V(j)'s slots has landed (the tail tile
-        // is the unit's last), so the parity waits below see V(j)'s own fills.
-        if (j >= 1)
+        // is the unit's last), so the parity waits below see V(j)'s own fills. The window's
+        // first tile and the sinks' last need not be the unit's last: K(j+1), loaded before
+        // V(j), has landed once S(j+1) is done (which does not wait for this P(j)).
+        if constexpr (WIN)
+          if (j + 1 < n)
+            ok = warp_wait(bar(C::B_SFULL + ((j + 1) & 1)), ((j + 1) >> 1) & 1, abort_flag, tmo);
+        if (ok && j >= 1)
           ok = warp_wait(bar(C::B_PVDONE + ((j - 1) & 1)), ((j - 1) >> 1) & 1, abort_flag, tmo);
         const uint32_t seq0 = v_item(j, n) * NP;
         for (int q = 0; q < NP && ok; ++q)
@@ -326,7 +333,13 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& tm_k, const CUten
         tmem_wait_ld();
 #pragma unroll
         for (int h = 0; h < 8; ++h)
-          if (h < G) base[(row0 + h) * D + 128 * hf + t] = o[h] * inv_l[h];
+          if (h < G) {
+            const int64_t at = (row0 + h) * D + 128 * hf + t;
+            if (WIN && !partial)
+              reinterpret_cast<uint16_t*>(a.out)[at] = to16<BF16>(o[h] * inv_l[h]);
+            else
+              base[at] = o[h] * inv_l[h];
+          }
       }
       if (partial) {
 #pragma unroll
@@ -337,10 +350,10 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& tm_k, const CUten
     }
   } else if (warp > kMmaWarp) {
     // ============================================================ TMA issuers (three warps)
-    kv_copy_role<NP, NSLOT, C::PANEL_LOG, true>(a, &tm_k, &tm_v, g, kt0, n, warp - kMmaWarp - 1,
-                                                sb + C::RING_OFF, bar(C::B_FULL),
-                                                bar(C::B_EMPTY), pre_row0, pre_row1, abort_flag,
-                                                tmo);
+    kv_copy_role<NP, NSLOT, C::PANEL_LOG, true, WIN>(a, &tm_k, &tm_v, g, kt0, n,
+                                                     warp - kMmaWarp - 1, sb + C::RING_OFF,
+                                                     bar(C::B_FULL), bar(C::B_EMPTY), pre_row0,
+                                                     pre_row1, abort_flag, tmo);
   } else {
     // ============================================================ MMA issuer (one lane)
     if (lane == 0) {
@@ -429,17 +442,17 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& tm_k, const CUten
   }
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool WIN>
 __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const PrefillArgs a) {
-  decode_body<D, BF16, false>(tm_k, tm_v, a, nullptr);
+  decode_body<D, BF16, false, WIN>(tm_k, tm_v, a, nullptr);
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool WIN>
 __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
     decode_batch_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a,
                         const __grid_constant__ ItemTable items) {
-  decode_body<D, BF16, true>(tm_k, tm_v, a, &items);
+  decode_body<D, BF16, true, WIN>(tm_k, tm_v, a, &items);
 }

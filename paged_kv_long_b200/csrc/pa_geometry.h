@@ -44,6 +44,27 @@ PA_HD int64_t tile_kv_tiles(int64_t qt, int64_t R, int G, int64_t H) {
   return ceil_div64(H + tile_last_token(qt, R, G) + 1, kTileKeys);
 }
 
+// ---- sliding window with sinks
+//
+// A row at position p sees key j <= p when j > p - window (its last `window` keys, its own
+// included) or j < sinks (the sequence's first keys, which stay visible). The rows of a unit at
+// positions p_first .. p_last together see keys [0, min(sinks, p_last + 1)) and
+// [lo, p_last], lo = max(0, p_first + 1 - window): two runs of KV tiles, which the unit walks as
+// one list of `n` tiles. Tile v of the list is KV tile v for v < head, else KV tile v + gap.
+PA_HD int64_t window_lo(int64_t p_first, int64_t window) {
+  const int64_t lo = p_first + 1 - window;
+  return lo > 0 ? lo : 0;
+}
+PA_HD void window_tiles(int64_t p_first, int64_t p_last, int64_t window, int64_t sinks,
+                        int64_t* head, int64_t* gap, int64_t* n) {
+  const int64_t n_end = p_last / kTileKeys + 1;
+  const int64_t w0 = window_lo(p_first, window) / kTileKeys;
+  const int64_t hs = ceil_div64(sinks < p_last + 1 ? sinks : p_last + 1, kTileKeys);
+  *head = hs;
+  *gap = hs < w0 ? w0 - hs : 0;
+  *n = n_end - *gap;
+}
+
 // KV tiles [*kt0, *kt1) of split s (of S) of a tile that sees n_kt KV tiles.
 PA_HD void split_range(int64_t n_kt, int s, int S, int64_t* kt0, int64_t* kt1) {
   *kt0 = (int64_t)s * n_kt / S;

@@ -25,7 +25,11 @@
 // combine_kernel: one warp per (row, head) merges the S partials with a log-sum-exp
 //   weighting (the "reduce" of splash PR #33); combine_blocks_kernel does the same for the
 //   cut row blocks of balanced plans.
+//   With a sliding window and sinks (the WIN instantiations of these kernels) a unit walks two
+//   runs of KV tiles, skips the pages between them, and writes a 16-bit output.
 // kv_append_kernel (kv_append.cuh): a chunk's K/V rows into their pages.
+// block_tables_kernel (step_tables.cuh): a step's page-table entries, positions and slots.
+// qk_rope_append_kernel (qk_rope.cuh): head norms, rotation and the cache write in one pass.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -94,7 +98,50 @@ struct PrefillArgs {
   // Batched prefill (balanced and batch > 0): an item's row block names its sequence (the item
   // table's sequence list); q_row0 is that sequence's first row in the packed Q / out arrays.
   int32_t q_row0;
+  // Sliding window with sinks (the WIN kernels; window_tiles): the row at position p sees key
+  // j <= p with j > p - window or j < sinks. Per unit: win_lo, the first key of its earliest
+  // row's window, and its tile list (unit tile v is KV tile v for v < tile_head, else
+  // v + tile_gap).
+  int64_t window, sinks;
+  int64_t win_lo, tile_head, tile_gap;
 };
+
+// KV tile of entry t of the unit's tile list.
+template <bool WIN>
+__device__ __forceinline__ int64_t kv_tile(const PrefillArgs& a, int64_t t) {
+  if constexpr (WIN) return t < a.tile_head ? t : t + a.tile_gap;
+  return t;
+}
+// No row of the unit sees key `key` (past the sequence, or between the sinks and win_lo).
+template <bool WIN>
+__device__ __forceinline__ bool key_unseen(const PrefillArgs& a, int64_t key) {
+  if constexpr (WIN)
+    return key >= a.total_keys || (key < a.win_lo && key >= a.sinks);
+  return key >= a.total_keys;
+}
+// The KV tile at key0 holds such a key. Its page may hold any bits there, and P is 0 for it,
+// but 0 * NaN is NaN inside the MMA, so the softmax warps zero those V rows first.
+template <bool WIN>
+__device__ __forceinline__ bool tile_unseen(const PrefillArgs& a, int64_t key0) {
+  if constexpr (WIN) {
+    const int64_t from = key0 > a.sinks ? key0 : a.sinks;
+    const int64_t to = key0 + kTileKeys < a.win_lo ? key0 + kTileKeys : a.win_lo;
+    return key0 + kTileKeys > a.total_keys || from < to;
+  }
+  return key0 + kTileKeys > a.total_keys;
+}
+// Tile list of a unit whose rows sit at positions p_first .. p_last.
+__device__ __forceinline__ void set_window(PrefillArgs& a, int64_t p_first, int64_t p_last) {
+  int64_t n;
+  a.win_lo = window_lo(p_first, a.window);
+  window_tiles(p_first, p_last, a.window, a.sinks, &a.tile_head, &a.tile_gap, &n);
+}
+// The output moved on by n elements: fp32, or 16-bit in the WIN kernels.
+template <bool WIN>
+__device__ __forceinline__ float* out_at(float* out, int64_t n) {
+  if constexpr (WIN) return reinterpret_cast<float*>(reinterpret_cast<uint16_t*>(out) + n);
+  return out + n;
+}
 
 // The work items of a balanced plan, passed by value (kernel parameter space): no device
 // allocation, and a CUDA graph that captures the launch keeps its own copy.
@@ -108,12 +155,12 @@ constexpr int kSlotUniform = -2;
 // Batched plans: point the arguments at the sequence that owns global row block rb (its Q and
 // output rows, its page-table row, its history and rows) and return the row block's number
 // within the sequence.
-template <int D>
+template <int D, bool WIN = false>
 __device__ __forceinline__ int32_t batch_rebase(PrefillArgs& a, const ItemTable& t, int32_t rb) {
   const int b = seq_of_rb(t.seq, a.batch, rb);
   const PaSeq sq = t.seq[b];
   a.q += (int64_t)sq.q_row0 * a.Hq * D;
-  a.out += (int64_t)sq.q_row0 * a.Hq * D;
+  a.out = out_at<WIN>(a.out, (int64_t)sq.q_row0 * a.Hq * D);
   a.page_table += (int64_t)b * a.table_stride;
   a.hist_len = sq.hist;
   a.R = sq.rows;
@@ -325,7 +372,7 @@ struct SoftmaxCtx {
 // together with its base-2 log-sum-exp. The row goes through shared memory (x.stage_off, idle
 // once the last P V is done; rows 16 bytes apart from a multiple of 128 so that a warp's
 // stores spread over the banks) and leaves as one contiguous bulk copy.
-template <int D>
+template <int D, bool WIN, bool BF16>
 __device__ __forceinline__ void write_row(const PrefillArgs& a, const SoftmaxCtx& x, int r,
                                           bool valid, int64_t tok, int head, float m_run,
                                           float l_run, uint32_t t_lane) {
@@ -335,13 +382,25 @@ __device__ __forceinline__ void write_row(const PrefillArgs& a, const SoftmaxCtx
     ws_row = (int64_t)x.slot * a.rows_per_block + x.row0 + r;
   else if (x.slot == kSlotUniform && a.splits > 1)
     ws_row = (int64_t)x.s * a.ws_split_rows + tok * a.Hq + head;
-  float* dst = ws_row < 0 ? a.out + (tok * a.Hq + head) * (int64_t)D : a.ws_o + ws_row * D;
+  float* dst = ws_row < 0 ? out_at<WIN>(a.out, (tok * a.Hq + head) * (int64_t)D)
+                          : a.ws_o + ws_row * D;
+  const bool half = WIN && ws_row < 0;  // a 16-bit output row, rounded here once
   const uint32_t srow = x.sb + x.stage_off + (uint32_t)r * (uint32_t)(D * 4 + 16);
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
     float o[32];
     tmem_ld32(t_lane + kOCol + 32u * c, o);
     tmem_wait_ld();
+    if (half) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        st_shared_v4(srow + 64u * c + 16u * i,
+                     pack2<BF16>(o[8 * i] * inv_l, o[8 * i + 1] * inv_l),
+                     pack2<BF16>(o[8 * i + 2] * inv_l, o[8 * i + 3] * inv_l),
+                     pack2<BF16>(o[8 * i + 4] * inv_l, o[8 * i + 5] * inv_l),
+                     pack2<BF16>(o[8 * i + 6] * inv_l, o[8 * i + 7] * inv_l));
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       st_shared_v4(srow + 128u * c + 16u * i, __float_as_uint(o[4 * i] * inv_l),
@@ -349,13 +408,27 @@ __device__ __forceinline__ void write_row(const PrefillArgs& a, const SoftmaxCtx
                    __float_as_uint(o[4 * i + 3] * inv_l));
   }
   fence_proxy_async_smem();
-  if (valid) bulk_store(dst, srow, D * 4);
+  if (valid) bulk_store(dst, srow, half ? D * 2 : D * 4);
   bulk_commit();
   bulk_wait_read_all();
   if (valid && ws_row >= 0) a.ws_lse[ws_row] = l_run > 0.f ? m_run + log2f(l_run) : -INFINITY;
 }
 
-template <int D, bool PAGED, bool BF16, bool SQ, class VTail>
+// The window's lower limit on a row's scores of the tile at key0, by select: keys below the
+// row's window (limit - window + 1 - key0 keys in, limit its last key) that are no sinks.
+__device__ __forceinline__ void mask_window(const PrefillArgs& a, int64_t limit, int64_t key0,
+                                            float (&sv)[kTileKeys]) {
+  const int64_t below = limit + 1 - a.window - key0;
+  if (below <= 0) return;
+  const int end = below < kTileKeys ? (int)below : kTileKeys;
+  const int64_t snk = a.sinks - key0;
+  const int first = snk < 0 ? 0 : snk < kTileKeys ? (int)snk : kTileKeys;
+#pragma unroll
+  for (int c = 0; c < kTileKeys; ++c)
+    if (c >= first && c < end) sv[c] = -INFINITY;
+}
+
+template <int D, bool PAGED, bool BF16, bool SQ, bool WIN, class VTail>
 __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const SoftmaxCtx& x,
                                              VTail&& v_tail) {
   constexpr int NP = D / 64;
@@ -409,7 +482,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Softmax
     for (int j = 0; j < n; ++j) {
       const int sbuf = j & 1;
       const uint32_t s_col = kSCol0 + 128u * sbuf;
-      const int64_t key0 = (kt0 + j) * kTileKeys;
+      const int64_t key0 = kv_tile<WIN>(a, kt0 + j) * kTileKeys;
       if (!warp_wait(x.bar_sfull + 8u * sbuf, (j >> 1) & 1, abort_flag, tmo)) {
         ok = false;
         break;
@@ -429,6 +502,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Softmax
         for (int c = 0; c < kTileKeys; ++c)
           if (c > rel) sv[c] = -INFINITY;
       }
+      if constexpr (WIN) mask_window(a, limit, key0, sv);
       // row max: eight independent chains, then a tree
       float mx8[8];
 #pragma unroll
@@ -490,8 +564,20 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Softmax
       }
 
       if constexpr (PAGED) {
-        if (key0 + kTileKeys > a.total_keys) {
-          const bool zero_me = key0 + r >= a.total_keys;
+        if (tile_unseen<WIN>(a, key0)) {
+          if constexpr (WIN) {
+            // Such a tile need not be the unit's last. Once S(j+1) and PV(j-1) are done, every
+            // earlier fill of V(j)'s slots has landed (K(0..j+1), V(0..j-1)), so the parity
+            // waits of v_tail see V(j)'s own fills. Neither wait needs this P(j).
+            if ((j + 1 < n && !warp_wait(x.bar_sfull + 8u * ((j + 1) & 1), ((j + 1) >> 1) & 1,
+                                         abort_flag, tmo)) ||
+                (j >= 1 && !warp_wait(x.bar_pvdone + 8u * ((j - 1) & 1), ((j - 1) >> 1) & 1,
+                                      abort_flag, tmo))) {
+              ok = false;
+              break;
+            }
+          }
+          const bool zero_me = key_unseen<WIN>(a, key0 + r);
           if (!v_tail(j, zero_me ? r : -1)) {
             ok = false;
             break;
@@ -504,7 +590,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Softmax
       // P lives in tensor memory: a CTA-scope release orders it (see mbar_arrive_remote_tc);
       // a tile whose V rows this thread zeroed in shared memory takes the cluster-scope one.
       if (lane == 0) {
-        if (x.remote_arrive && !(PAGED && key0 + kTileKeys > a.total_keys))
+        if (x.remote_arrive && !(PAGED && tile_unseen<WIN>(a, key0)))
           mbar_arrive_remote_tc(x.arrive_pfull + 8u * sbuf);
         else
           arrive(x.arrive_pfull + 8u * sbuf);
@@ -516,22 +602,32 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Softmax
     if (ok) ok = warp_wait(x.bar_pvdone + 8u * ((n - 1) & 1), ((n - 1) >> 1) & 1, abort_flag, tmo);
     if (ok) {
       tc_fence_after();
-      write_row<D>(a, x, r, valid, tok, head, m_run, l_run, t_lane);
+      write_row<D, WIN, BF16>(a, x, r, valid, tok, head, m_run, l_run, t_lane);
     }
   }
+}
+
+// Some row of the unit sees a key of logical page lp (of those below its last key).
+template <bool WIN>
+__device__ __forceinline__ bool page_seen(const PrefillArgs& a, int64_t lp) {
+  if constexpr (WIN)
+    return (lp << a.page_shift) < a.sinks || ((lp + 1) << a.page_shift) > a.win_lo;
+  return true;
 }
 
 // Key-row coordinate in the pool of page `lane` (< pages per tile) of KV tile kt0 + jt of a
 // unit with n tiles: page_table[page] << page_shift, or oob_row (the TMA fills zeros there)
 // past the unit or the table; an entry outside the pool is reported (by `report` lanes) and
 // read as oob_row. Contiguous K/V: the tile's first key row.
-template <bool PAGED>
+// WIN: pages between the sinks and the unit's window are not read (their table entries may hold
+// anything) and arrive as zeros.
+template <bool PAGED, bool WIN = false>
 __device__ __forceinline__ int32_t tile_page_row(const PrefillArgs& a, int64_t kt0, int n,
                                                  int jt, int lane, bool report) {
   int32_t row = a.oob_row;
   if constexpr (PAGED) {
-    const int64_t lp = (kt0 + jt) * a.pages_per_tile + lane;
-    if (jt < n && lane < a.pages_per_tile && lp < a.table_len) {
+    const int64_t lp = kv_tile<WIN>(a, kt0 + jt) * a.pages_per_tile + lane;
+    if (jt < n && lane < a.pages_per_tile && lp < a.table_len && page_seen<WIN>(a, lp)) {
       const int32_t e = __ldg(a.page_table + lp);
       if (e >= 0 && e < a.num_pages)
         row = e << a.page_shift;
@@ -550,14 +646,17 @@ __device__ __forceinline__ int32_t tile_page_row(const PrefillArgs& a, int64_t k
 // tiles [kt0, kt1). A length outside 0 .. the table row's keys is reported like a bad page
 // entry and clamped. Every thread of the block takes part (block barriers in the ranking);
 // `scratch`: shared memory that no copy writes yet (see seq_of_rank).
-template <int D>
+// WIN: the blocks take the sequences in order (most windows are full, so their units are alike
+// and the ranking would only delay them), and the tiles split are the window's and the sinks'.
+template <int D, bool WIN = false>
 __device__ __forceinline__ void decode_unit(PrefillArgs& a, int32_t* scratch, int* g, int* s,
                                             int64_t* kt0, int64_t* kt1) {
   const int64_t per_seq = (int64_t)a.Hkv * a.splits;
   const int64_t rem = blockIdx.x % per_seq;
   int64_t b = blockIdx.x / per_seq;
-  b = a.batch <= kRankedSeqsMax ? seq_of_rank(a.seq_lens, a.batch, (int)b, scratch)
-                                : seq_of_class_rank(a.seq_lens, a.batch, (int)b, scratch);
+  if constexpr (!WIN)
+    b = a.batch <= kRankedSeqsMax ? seq_of_rank(a.seq_lens, a.batch, (int)b, scratch)
+                                  : seq_of_class_rank(a.seq_lens, a.batch, (int)b, scratch);
   *g = (int)(rem / a.splits);
   *s = (int)(rem % a.splits);
   int64_t len = __ldg(a.seq_lens + b);
@@ -567,7 +666,7 @@ __device__ __forceinline__ void decode_unit(PrefillArgs& a, int32_t* scratch, in
     len = len < 0 ? 0 : cap;
   }
   a.q += b * a.Hq * D;
-  a.out += b * a.Hq * D;
+  a.out = out_at<WIN>(a.out, b * a.Hq * D);
   if (a.ws_o) {
     a.ws_o += b * a.Hq * D;
     a.ws_lse += b * a.Hq;
@@ -577,12 +676,21 @@ __device__ __forceinline__ void decode_unit(PrefillArgs& a, int32_t* scratch, in
   a.total_keys = len;
   a.table_len = (len + a.page_rows - 1) / a.page_rows;
   a.R = len > 0 ? 1 : 0;
+  if constexpr (WIN) {
+    int64_t n = 0;
+    if (len > 0) {
+      a.win_lo = window_lo(len - 1, a.window);
+      window_tiles(len - 1, len - 1, a.window, a.sinks, &a.tile_head, &a.tile_gap, &n);
+    }
+    split_range(n, *s, a.splits, kt0, kt1);
+    return;
+  }
   split_range((len + kTileKeys - 1) / kTileKeys, *s, a.splits, kt0, kt1);
 }
 
 // A unit without KV tiles (a split past its tile's keys, or a decode sequence with no key):
 // zeros for the output (one split) or an empty partial (zeros, LSE -inf), by threads < 128.
-template <int D>
+template <int D, bool WIN = false>
 __device__ __forceinline__ void empty_unit(const PrefillArgs& a, int64_t qt, int g, int s) {
   if (threadIdx.x >= kTileRows) return;
   const int64_t grow = qt * kTileRows + threadIdx.x;
@@ -590,8 +698,8 @@ __device__ __forceinline__ void empty_unit(const PrefillArgs& a, int64_t qt, int
   if (tok >= (a.batch > 0 ? 1 : a.R)) return;
   const int head = g * a.G + (int)(grow % a.G);
   if (a.splits == 1) {
-    float4* d4 = reinterpret_cast<float4*>(a.out + (tok * a.Hq + head) * D);
-    for (int i = 0; i < D / 4; ++i) d4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4* d4 = reinterpret_cast<float4*>(out_at<WIN>(a.out, (tok * a.Hq + head) * D));
+    for (int i = 0; i < (WIN ? D / 8 : D / 4); ++i) d4[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   } else {
     const int64_t row = (int64_t)s * a.ws_split_rows + tok * a.Hq + head;
     float4* d4 = reinterpret_cast<float4*>(a.ws_o + row * D);
@@ -605,7 +713,7 @@ __device__ __forceinline__ void empty_unit(const PrefillArgs& a, int64_t qt, int
 // kt0 .. kt0 + n - 1 of KV head g, fill number q by warp q % kIssuers. full[i] / empty[i] are the slots'
 // barriers (8 bytes apart). pre_row0 / pre_row1: lane i's page row of tiles 0 / 1 (read
 // before the set-up). Every copy has landed when this returns.
-template <int NP, int NSLOT, int PANEL_LOG, bool PAGED>
+template <int NP, int NSLOT, int PANEL_LOG, bool PAGED, bool WIN = false>
 __device__ __forceinline__ void kv_copy_role(const PrefillArgs& a, const CUtensorMap* tm_k,
                                              const CUtensorMap* tm_v, int g, int64_t kt0, int n,
                                              int w, uint32_t ring, uint32_t bar_full, uint32_t bar_empty,
@@ -624,8 +732,8 @@ __device__ __forceinline__ void kv_copy_role(const PrefillArgs& a, const CUtenso
   auto fetch = [&](int jt) -> int32_t {
     int32_t row = a.oob_row;
     if constexpr (PAGED) {
-      const int64_t lp = (kt0 + jt) * ppt + lane;
-      if (jt < n && lane < ppt && lp < a.table_len) {
+      const int64_t lp = kv_tile<WIN>(a, kt0 + jt) * ppt + lane;
+      if (jt < n && lane < ppt && lp < a.table_len && page_seen<WIN>(a, lp)) {
         const int32_t e = __ldg(a.page_table + lp);
         if (e >= 0 && e < a.num_pages)
           row = e << a.page_shift;
@@ -694,7 +802,7 @@ __device__ __forceinline__ void kv_copy_role(const PrefillArgs& a, const CUtenso
 }
 
 // ---------------------------------------------------------------- prefill kernel
-template <int D, bool PAGED, bool BF16, bool SQ>
+template <int D, bool PAGED, bool BF16, bool SQ, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const PrefillArgs a_in, const __grid_constant__ ItemTable items) {
@@ -711,14 +819,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   int g, s, slot = kSlotUniform;
   if (a.balanced) {
     const PaItem it = items.item[blockIdx.x];
-    const int32_t rb = a.batch > 0 ? batch_rebase<D>(a, items, it.rb) : it.rb;
+    const int32_t rb = a.batch > 0 ? batch_rebase<D, WIN>(a, items, it.rb) : it.rb;
     rb_coords(rb, a.q_tiles, a.Hkv, &qt, &g);
     s = 0;
     kt0 = it.kt0;
     kt1 = it.kt1;
     slot = it.slot;
+    if constexpr (WIN)
+      set_window(a, a.hist_len + tile_first_token(qt, a.G),
+                 a.hist_len + tile_last_token(qt, a.R, a.G));
   } else if (a.batch > 0) {
-    decode_unit<D>(a, reinterpret_cast<int32_t*>(smem + C::RING_OFF), &g, &s, &kt0, &kt1);
+    decode_unit<D, WIN>(a, reinterpret_cast<int32_t*>(smem + C::RING_OFF), &g, &s, &kt0, &kt1);
     qt = 0;
   } else {
     unit_coords(blockIdx.x, a.q_tiles, a.Hkv, a.splits, &qt, &g, &s);
@@ -727,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n = (int)(kt1 - kt0);
 
   if (n == 0) {  // a split past this tile's keys (only when S > KV tiles): empty partial
-    empty_unit<D>(a, qt, g, s);
+    empty_unit<D, WIN>(a, qt, g, s);
     return;
   }
 
@@ -736,8 +847,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t pre_row0 = a.oob_row, pre_row1 = a.oob_row;
   if (warp > kMmaWarp) {
     const bool report = warp == kMmaWarp + 1;
-    pre_row0 = tile_page_row<PAGED>(a, kt0, n, 0, lane, report);
-    pre_row1 = tile_page_row<PAGED>(a, kt0, n, 1, lane, report);
+    pre_row0 = tile_page_row<PAGED, WIN>(a, kt0, n, 0, lane, report);
+    pre_row1 = tile_page_row<PAGED, WIN>(a, kt0, n, 1, lane, report);
   }
   auto bar = [&](int i) -> uint32_t { return sb + C::BAR_OFF + 8u * (uint32_t)i; };
   auto slot_addr = [&](uint32_t slot) -> uint32_t { return sb + C::RING_OFF + slot * kPanel; };
@@ -815,10 +926,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       return true;
     };
-    softmax_role<D, PAGED, BF16, SQ>(a, sc, v_tail);
+    softmax_role<D, PAGED, BF16, SQ, WIN>(a, sc, v_tail);
   } else if (warp > kMmaWarp) {
     // ============================================================ TMA issuers (three warps)
-    kv_copy_role<NP, NSLOT, C::PANEL_LOG, PAGED>(a, &tm_k, &tm_v, g, kt0, n,
+    kv_copy_role<NP, NSLOT, C::PANEL_LOG, PAGED, WIN>(a, &tm_k, &tm_v, g, kt0, n,
                                                  warp - kMmaWarp - 1, sb + C::RING_OFF,
                                                  bar(C::B_FULL), bar(C::B_EMPTY), pre_row0,
                                                  pre_row1, abort_flag, tmo);
@@ -910,6 +1021,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #include "prefill_pair.cuh"
 #include "decode_kernel.cuh"
 #include "kv_append.cuh"
+#include "step_tables.cuh"
+#include "qk_rope.cuh"
 
 // ---------------------------------------------------------------- combine kernels
 // The merge of one output row (one warp): part p's partial row is at o + p * o_stride (D fp32,
@@ -920,7 +1033,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // before the weights are known: one memory latency per four parts, not one per part and pass.
 // Every lane takes part in every shuffle (at D = 64 only lanes 0-15 own columns, but the
 // weights of parts 16-31 sit in lanes 16-31).
-template <int NPASS>  // 128-column passes: 1 for D = 64 and 128, 2 for D = 256
+// OUT: the row's type at dst, fp32 or (rounded once) f16 or bf16.
+constexpr int kOutF32 = 0, kOutF16 = 1, kOutBf16 = 2;
+
+template <int NPASS, int OUT>  // 128-column passes: 1 for D = 64 and 128, 2 for D = 256
 __device__ __forceinline__ void merge_row(const float* __restrict__ o, int64_t o_stride,
                                           const float* __restrict__ lse_p, int64_t lse_stride,
                                           int np, int D, float* __restrict__ dst, int lane) {
@@ -969,13 +1085,19 @@ __device__ __forceinline__ void merge_row(const float* __restrict__ o, int64_t o
 #pragma unroll
   for (int ps = 0; ps < NPASS; ++ps) {
     const int d0 = lane * 4 + 128 * ps;
-    if (d0 < D)
+    if (d0 >= D) continue;
+    if constexpr (OUT == kOutF32)
       *reinterpret_cast<float4*>(dst + d0) = make_float4(acc[ps].x * inv, acc[ps].y * inv,
                                                          acc[ps].z * inv, acc[ps].w * inv);
+    else
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(dst) + d0) =
+          make_uint2(pack2<OUT == kOutBf16>(acc[ps].x * inv, acc[ps].y * inv),
+                     pack2<OUT == kOutBf16>(acc[ps].z * inv, acc[ps].w * inv));
   }
 }
 
 // Uniform splits: one warp per (row, head) merges its S <= 32 split partials into out.
+template <int OUT>
 __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ ws_o,
                                                       const float* __restrict__ ws_lse,
                                                       float* __restrict__ out, int S, int64_t RH,
@@ -983,10 +1105,11 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
   const int64_t w = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
   if (w >= RH) return;
   const int lane = threadIdx.x & 31;
+  float* dst = out_at<OUT != kOutF32>(out, w * D);
   if (D == 256)
-    merge_row<2>(ws_o + w * D, RH * D, ws_lse + w, RH, S, D, out + w * D, lane);
+    merge_row<2, OUT>(ws_o + w * D, RH * D, ws_lse + w, RH, S, D, dst, lane);
   else
-    merge_row<1>(ws_o + w * D, RH * D, ws_lse + w, RH, S, D, out + w * D, lane);
+    merge_row<1, OUT>(ws_o + w * D, RH * D, ws_lse + w, RH, S, D, dst, lane);
 }
 
 // Balanced plans: one warp per packed row of a cut row block merges that row's parts (workspace
@@ -997,6 +1120,7 @@ struct SplitTable {
   PaSeq seq[kMaxSeqs];
 };
 
+template <int OUT>
 __global__ void __launch_bounds__(256) combine_blocks_kernel(
     const float* __restrict__ ws_o, const float* __restrict__ ws_lse, float* __restrict__ out,
     const __grid_constant__ SplitTable t, int n_blocks, int rows_per_block, int64_t q_units,
@@ -1012,7 +1136,7 @@ __global__ void __launch_bounds__(256) combine_blocks_kernel(
     rb -= sq.rb0;
     R = sq.rows;
     q_units = ceil_div64(q_tiles_for(sq.rows, G), rows_per_block / kTileRows);
-    out += (int64_t)sq.q_row0 * Hq * D;
+    out = out_at<OUT != kOutF32>(out, (int64_t)sq.q_row0 * Hq * D);
   }
   int64_t qu;
   int g;
@@ -1022,12 +1146,12 @@ __global__ void __launch_bounds__(256) combine_blocks_kernel(
   if (tok >= R) return;
   const int head = g * G + (int)(grow % G);
   const int64_t row0 = (int64_t)b.first_slot * rows_per_block + lr;  // part p: row0 + p * rpb
-  float* dst = out + (tok * Hq + head) * (int64_t)D;
+  float* dst = out_at<OUT != kOutF32>(out, (tok * Hq + head) * (int64_t)D);
   const int64_t rpb = rows_per_block;
   if (D == 256)
-    merge_row<2>(ws_o + row0 * D, rpb * D, ws_lse + row0, rpb, b.nparts, D, dst, lane);
+    merge_row<2, OUT>(ws_o + row0 * D, rpb * D, ws_lse + row0, rpb, b.nparts, D, dst, lane);
   else
-    merge_row<1>(ws_o + row0 * D, rpb * D, ws_lse + row0, rpb, b.nparts, D, dst, lane);
+    merge_row<1, OUT>(ws_o + row0 * D, rpb * D, ws_lse + row0, rpb, b.nparts, D, dst, lane);
 }
 
 // ---------------------------------------------------------------- timeout self-test
@@ -1117,10 +1241,10 @@ bool make_q_map(CUtensorMap* map, const void* base, bool bf16, int D, int G, int
   return r == CUDA_SUCCESS;
 }
 
-template <int D, bool PAGED, bool BF16, bool SQ = false>
+template <int D, bool PAGED, bool BF16, bool SQ = false, bool WIN = false>
 cudaError_t launch_prefill(int64_t grid, cudaStream_t st, const CUtensorMap& tk,
                            const CUtensorMap& tv, const PrefillArgs& a, const ItemTable& it) {
-  auto kern = prefill_kernel<D, PAGED, BF16, SQ>;
+  auto kern = prefill_kernel<D, PAGED, BF16, SQ, WIN>;
   static std::atomic<uint64_t> configured{0};  // one bit per device ordinal
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1136,11 +1260,11 @@ cudaError_t launch_prefill(int64_t grid, cudaStream_t st, const CUtensorMap& tk,
   return cudaGetLastError();
 }
 
-template <bool PAGED, bool BF16>
+template <bool PAGED, bool BF16, bool WIN = false>
 cudaError_t launch_pair(int64_t grid, cudaStream_t st, const CUtensorMap& tk,
                         const CUtensorMap& tv, const CUtensorMap& tq, const PrefillArgs& a,
                         const ItemTable& it) {
-  auto kern = prefill_pair_kernel<PAGED, BF16>;
+  auto kern = prefill_pair_kernel<PAGED, BF16, WIN>;
   static std::atomic<uint64_t> configured{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1197,53 +1321,54 @@ cudaError_t configure_decode(K kern, int smem, std::atomic<uint64_t>& configured
   return cudaSuccess;
 }
 
-template <int D, bool BF16, bool BAL>
+template <int D, bool BF16, bool BAL, bool WIN>
 cudaError_t launch_decode(int64_t grid, cudaStream_t st, const CUtensorMap& tk,
                           const CUtensorMap& tv, const PrefillArgs& a, const ItemTable& it) {
   static std::atomic<uint64_t> configured{0};  // one bit per device ordinal
   cudaError_t e;
   if constexpr (BAL) {
-    e = configure_decode(decode_batch_kernel<D, BF16>, DecCfg<D>::LAUNCH_SMEM, configured);
+    e = configure_decode(decode_batch_kernel<D, BF16, WIN>, DecCfg<D>::LAUNCH_SMEM, configured);
     if (e != cudaSuccess) return e;
-    decode_batch_kernel<D, BF16><<<(unsigned)grid, kThreads, DecCfg<D>::LAUNCH_SMEM, st>>>(
+    decode_batch_kernel<D, BF16, WIN><<<(unsigned)grid, kThreads, DecCfg<D>::LAUNCH_SMEM, st>>>(
         tk, tv, a, it);
   } else {
-    e = configure_decode(decode_kernel<D, BF16>, DecCfg<D>::LAUNCH_SMEM, configured);
+    e = configure_decode(decode_kernel<D, BF16, WIN>, DecCfg<D>::LAUNCH_SMEM, configured);
     if (e != cudaSuccess) return e;
-    decode_kernel<D, BF16><<<(unsigned)grid, kThreads, DecCfg<D>::LAUNCH_SMEM, st>>>(tk, tv, a);
+    decode_kernel<D, BF16, WIN><<<(unsigned)grid, kThreads, DecCfg<D>::LAUNCH_SMEM, st>>>(tk, tv, a);
   }
   return cudaGetLastError();
 }
 
-template <bool BAL>
+template <bool BAL, bool WIN = false>
 cudaError_t launch_decode_d(int D, bool bf16, int64_t grid, cudaStream_t st,
                             const CUtensorMap& tk, const CUtensorMap& tv, const PrefillArgs& a,
                             const ItemTable& it) {
-  return D == 128 ? (bf16 ? launch_decode<128, true, BAL>(grid, st, tk, tv, a, it)
-                          : launch_decode<128, false, BAL>(grid, st, tk, tv, a, it))
-                  : (bf16 ? launch_decode<256, true, BAL>(grid, st, tk, tv, a, it)
-                          : launch_decode<256, false, BAL>(grid, st, tk, tv, a, it));
+  return D == 128 ? (bf16 ? launch_decode<128, true, BAL, WIN>(grid, st, tk, tv, a, it)
+                          : launch_decode<128, false, BAL, WIN>(grid, st, tk, tv, a, it))
+                  : (bf16 ? launch_decode<256, true, BAL, WIN>(grid, st, tk, tv, a, it)
+                          : launch_decode<256, false, BAL, WIN>(grid, st, tk, tv, a, it));
 }
 
 // Paged single-CTA launches of decode and batches (sq: every Q tile holds <= 8 packed rows).
+template <int D, bool WIN>
+cudaError_t launch_paged_single_d(bool bf16, bool sq, int64_t grid, cudaStream_t st,
+                                  const CUtensorMap& tk, const CUtensorMap& tv,
+                                  const PrefillArgs& a, const ItemTable& it) {
+  if (sq)
+    return bf16 ? launch_prefill<D, true, true, true, WIN>(grid, st, tk, tv, a, it)
+                : launch_prefill<D, true, false, true, WIN>(grid, st, tk, tv, a, it);
+  return bf16 ? launch_prefill<D, true, true, false, WIN>(grid, st, tk, tv, a, it)
+              : launch_prefill<D, true, false, false, WIN>(grid, st, tk, tv, a, it);
+}
+
+template <bool WIN = false>
 cudaError_t launch_paged_single(int D, bool bf16, bool sq, int64_t grid, cudaStream_t st,
                                 const CUtensorMap& tk, const CUtensorMap& tv,
                                 const PrefillArgs& a, const ItemTable& it) {
-  if (sq) {
-    switch (D) {
-      case 64: return bf16 ? launch_prefill<64, true, true, true>(grid, st, tk, tv, a, it)
-                           : launch_prefill<64, true, false, true>(grid, st, tk, tv, a, it);
-      case 128: return bf16 ? launch_prefill<128, true, true, true>(grid, st, tk, tv, a, it)
-                            : launch_prefill<128, true, false, true>(grid, st, tk, tv, a, it);
-      default: return bf16 ? launch_prefill<256, true, true, true>(grid, st, tk, tv, a, it)
-                           : launch_prefill<256, true, false, true>(grid, st, tk, tv, a, it);
-    }
-  }
   switch (D) {
-    case 64: return launch_d<64>(true, bf16, grid, st, tk, tv, a, it);
-    case 128: return launch_d<128>(true, bf16, grid, st, tk, tv, a, it);
-    default: return bf16 ? launch_prefill<256, true, true>(grid, st, tk, tv, a, it)
-                         : launch_prefill<256, true, false>(grid, st, tk, tv, a, it);
+    case 64: return launch_paged_single_d<64, WIN>(bf16, sq, grid, st, tk, tv, a, it);
+    case 128: return launch_paged_single_d<128, WIN>(bf16, sq, grid, st, tk, tv, a, it);
+    default: return launch_paged_single_d<256, WIN>(bf16, sq, grid, st, tk, tv, a, it);
   }
 }
 
@@ -1373,12 +1498,14 @@ extern "C" int pa_prefill(const pa_plan_t* plan, const void* q, const void* k_po
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-extern "C" int pa_decode(const pa_plan_t* plan, const void* q, const void* k_pool,
-                         const void* v_pool, const int32_t* block_table, int table_stride,
-                         const int32_t* seq_lens, int64_t num_pages, float* out, float* lse_ws,
-                         uint64_t ws_bytes, pa_stream_t stream) {
+// pa_decode (out fp32), and pa_window_decode's attention with a window (out of the input type).
+static int run_decode(const pa_plan_t* plan, const Window* win, const void* q,
+                      const void* k_pool, const void* v_pool, const int32_t* block_table,
+                      int table_stride, const int32_t* seq_lens, int64_t num_pages, float* out,
+                      float* lse_ws, uint64_t ws_bytes, pa_stream_t stream) {
   if (!plan || plan->batch <= 0 || plan->chunk_rows != plan->batch || plan->q_tiles != 1 ||
-      plan->policy == PA_POLICY_BALANCED)  // batch plans run through pa_batch_prefill
+      plan->policy == PA_POLICY_BALANCED ||  // batch plans run through pa_batch_prefill
+      plan->policy == PA_POLICY_WINDOW || (plan->policy == PA_POLICY_WINDOW_DECODE) != !!win)
     return PA_ERR_INVALID_ARG;
   if (!q || !k_pool || !v_pool || !block_table || !seq_lens || !out || table_stride <= 0 ||
       num_pages <= 0)
@@ -1428,22 +1555,56 @@ extern "C" int pa_decode(const pa_plan_t* plan, const void* q, const void* k_poo
   a.batch = B;
   a.table_stride = table_stride;
   a.seq_lens = seq_lens;
+  if (win) {
+    a.window = win->window;
+    a.sinks = win->sinks;
+  }
   thread_local ItemTable table;  // unused by decode units
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int64_t grid = plan->units;
   if (grid >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
   cudaError_t e;
   if (decode_swapped(D, plan->group))
-    e = launch_decode_d<false>(D, bf16, grid, st, tk, tv, a, table);
+    e = win ? launch_decode_d<false, true>(D, bf16, grid, st, tk, tv, a, table)
+            : launch_decode_d<false>(D, bf16, grid, st, tk, tv, a, table);
   else
-    e = launch_paged_single(D, bf16, plan->group <= 8, grid, st, tk, tv, a, table);
+    e = win ? launch_paged_single<true>(D, bf16, plan->group <= 8, grid, st, tk, tv, a, table)
+            : launch_paged_single(D, bf16, plan->group <= 8, grid, st, tk, tv, a, table);
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+extern "C" int pa_decode(const pa_plan_t* plan, const void* q, const void* k_pool,
+                         const void* v_pool, const int32_t* block_table, int table_stride,
+                         const int32_t* seq_lens, int64_t num_pages, float* out, float* lse_ws,
+                         uint64_t ws_bytes, pa_stream_t stream) {
+  return run_decode(plan, nullptr, q, k_pool, v_pool, block_table, table_stride, seq_lens,
+                    num_pages, out, lse_ws, ws_bytes, stream);
+}
+
+extern "C" int pa_window_decode(const pa_plan_t* plan, int window, int n_sinks, const void* q,
+                                const void* k_pool, const void* v_pool,
+                                const int32_t* block_table, int table_stride,
+                                const int32_t* seq_lens, int64_t num_pages, void* out,
+                                float* lse_ws, uint64_t ws_bytes, pa_stream_t stream) {
+  if (window < 1 || n_sinks < 0) return PA_ERR_INVALID_ARG;
+  const Window win{window, n_sinks};
+  const int st = run_decode(plan, &win, q, k_pool, v_pool, block_table, table_stride, seq_lens,
+                            num_pages, static_cast<float*>(out), lse_ws, ws_bytes, stream);
+  if (st != PA_OK || plan->splits == 1) return st;
+  const int64_t RH = (int64_t)plan->batch * plan->n_q_heads;
+  const float* ws_lse = lse_ws + (int64_t)plan->splits * RH * plan->head_dim;
+  auto merge = plan->dtype == PA_BF16 ? combine_kernel<kOutBf16> : combine_kernel<kOutF16>;
+  merge<<<(unsigned)((RH + 7) / 8), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+      lse_ws, ws_lse, static_cast<float*>(out), plan->splits, RH, plan->head_dim);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+
 extern "C" int pa_combine(const pa_plan_t* plan, const float* lse_ws, uint64_t ws_bytes,
                           float* out, pa_stream_t stream) {
-  if (!plan || (plan->policy == PA_POLICY_BALANCED && plan->batch != 0))
-    return PA_ERR_INVALID_ARG;  // batched plans merge with pa_batch_combine
+  if (!plan || (plan->policy == PA_POLICY_BALANCED && plan->batch != 0) ||
+      plan->policy == PA_POLICY_WINDOW || plan->policy == PA_POLICY_WINDOW_DECODE)
+    return PA_ERR_INVALID_ARG;  // batched plans merge with pa_batch_combine, windowed ones alone
   const int S = plan->splits;
   if (plan->policy == PA_POLICY_BALANCED) {
     Schedule sch;
@@ -1459,7 +1620,7 @@ extern "C" int pa_combine(const pa_plan_t* plan, const float* lse_ws, uint64_t w
     const int per = plan->ctas_per_unit;
     const int64_t q_units = ((int64_t)plan->q_tiles + per - 1) / per;
     const int64_t warps = (int64_t)sch.split.size() * sch.rows_per_block;
-    combine_blocks_kernel<<<(unsigned)((warps + 7) / 8), 256, 0,
+    combine_blocks_kernel<kOutF32><<<(unsigned)((warps + 7) / 8), 256, 0,
                             reinterpret_cast<cudaStream_t>(stream)>>>(
         lse_ws, lse_ws + (int64_t)sch.n_slots * sch.rows_per_block * D, out, table,
         (int)sch.split.size(), sch.rows_per_block, q_units, plan->n_kv_heads, plan->group,
@@ -1475,7 +1636,7 @@ extern "C" int pa_combine(const pa_plan_t* plan, const float* lse_ws, uint64_t w
   const float* ws_o = lse_ws;
   const float* ws_lse = lse_ws + (int64_t)S * RH * D;
   const int64_t blocks = (RH + 7) / 8;
-  combine_kernel<<<(unsigned)blocks, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+  combine_kernel<kOutF32><<<(unsigned)blocks, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
       ws_o, ws_lse, out, S, RH, D);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -1483,9 +1644,10 @@ extern "C" int pa_combine(const pa_plan_t* plan, const float* lse_ws, uint64_t w
 // ---------------------------------------------------------------- batched prefill
 namespace pa {
 // The batch and its schedule, rebuilt from the caller's lengths and checked against the plan.
-static int rebuild_batch(const pa_plan_t* plan, const int32_t* q_lens, const int64_t* hist_lens,
-                         Batch* bt, Schedule* sch) {
-  if (!plan || plan->batch <= 0 || plan->policy != PA_POLICY_BALANCED || !q_lens || !hist_lens)
+static int rebuild_batch(const pa_plan_t* plan, const Window* win, const int32_t* q_lens,
+                         const int64_t* hist_lens, Batch* bt, Schedule* sch) {
+  if (!plan || plan->batch <= 0 ||
+      plan->policy != (win ? PA_POLICY_WINDOW : PA_POLICY_BALANCED) || !q_lens || !hist_lens)
     return PA_ERR_INVALID_ARG;
   if (plan->batch > kMaxSeqs) return PA_ERR_UNSUPPORTED;
   const int D = plan->head_dim;
@@ -1497,7 +1659,7 @@ static int rebuild_batch(const pa_plan_t* plan, const int32_t* q_lens, const int
                                 plan->ctas_per_unit, bt);
   if (st != PA_OK) return st;
   if (!build_batch(plan->num_sms, D, plan->ctas_per_unit, plan->group, plan->n_kv_heads, *bt,
-                   sch) ||
+                   sch, win) ||
       (int64_t)sch->items.size() != plan->units || bt->total_rows != plan->chunk_rows ||
       (uint64_t)sch->n_slots * sch->rows_per_block * (D + 1) * 4ull != plan->ws_bytes)
     return PA_ERR_INVALID_ARG;
@@ -1505,15 +1667,12 @@ static int rebuild_batch(const pa_plan_t* plan, const int32_t* q_lens, const int
 }
 }  // namespace pa
 
-extern "C" int pa_batch_prefill(const pa_plan_t* plan, const int32_t* q_lens,
-                                const int64_t* hist_lens, const void* q, const void* k_pool,
-                                const void* v_pool, const int32_t* block_table, int table_stride,
-                                int64_t num_pages, float* out, float* lse_ws, uint64_t ws_bytes,
-                                pa_stream_t stream) {
-  Batch bt;
-  Schedule sch;
-  const int st = rebuild_batch(plan, q_lens, hist_lens, &bt, &sch);
-  if (st != PA_OK) return st;
+// The attention launch of a batch whose schedule is rebuilt: pa_batch_prefill (out fp32) and,
+// with a window, pa_window_prefill (out of the input type).
+static int run_batch(const pa_plan_t* plan, const Window* win, const Batch& bt,
+                     const Schedule& sch, const void* q, const void* k_pool, const void* v_pool,
+                     const int32_t* block_table, int table_stride, int64_t num_pages, float* out,
+                     float* lse_ws, uint64_t ws_bytes, pa_stream_t stream) {
   if (!q || !k_pool || !v_pool || !block_table || !out || table_stride <= 0 || num_pages <= 0)
     return PA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
@@ -1568,6 +1727,10 @@ extern "C" int pa_batch_prefill(const pa_plan_t* plan, const int32_t* q_lens,
   a.k_atoms = k_atoms ? 1 : 0;
   a.batch = plan->batch;
   a.table_stride = table_stride;
+  if (win) {
+    a.window = win->window;
+    a.sinks = win->sinks;
+  }
   thread_local ItemTable table;
   for (size_t i = 0; i < sch.items.size(); ++i) table.item[i] = sch.items[i];
   for (size_t i = 0; i < bt.seq.size(); ++i) table.seq[i] = bt.seq[i];
@@ -1576,24 +1739,45 @@ extern "C" int pa_batch_prefill(const pa_plan_t* plan, const int32_t* q_lens,
   int max_rows = 0;  // small Q when no sequence's Q tile holds more than 8 packed rows
   for (const PaSeq& sq : bt.seq) max_rows = std::max(max_rows, (int)sq.rows);
   const bool small_q = (int64_t)max_rows * plan->group <= 8;
+  const bool swapped =
+      batch_decode_swapped(D, plan->group, per, bt.seq.data(), (int)bt.seq.size());
   cudaError_t e;
-  if (per == 2)
+  if (win) {
+    if (per == 2)
+      e = bf16 ? launch_pair<true, true, true>(grid, cs, tk, tv, tq, a, table)
+               : launch_pair<true, false, true>(grid, cs, tk, tv, tq, a, table);
+    else if (swapped)
+      e = launch_decode_d<true, true>(D, bf16, grid, cs, tk, tv, a, table);
+    else
+      e = launch_paged_single<true>(D, bf16, small_q, grid, cs, tk, tv, a, table);
+  } else if (per == 2) {
     e = bf16 ? launch_pair<true, true>(grid, cs, tk, tv, tq, a, table)
              : launch_pair<true, false>(grid, cs, tk, tv, tq, a, table);
-  else if (batch_decode_swapped(D, plan->group, per, bt.seq.data(), (int)bt.seq.size()))
+  } else if (swapped) {
     e = launch_decode_d<true>(D, bf16, grid, cs, tk, tv, a, table);
-  else
+  } else {
     e = launch_paged_single(D, bf16, small_q, grid, cs, tk, tv, a, table);
+  }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-extern "C" int pa_batch_combine(const pa_plan_t* plan, const int32_t* q_lens,
-                                const int64_t* hist_lens, const float* lse_ws, uint64_t ws_bytes,
-                                float* out, pa_stream_t stream) {
+extern "C" int pa_batch_prefill(const pa_plan_t* plan, const int32_t* q_lens,
+                                const int64_t* hist_lens, const void* q, const void* k_pool,
+                                const void* v_pool, const int32_t* block_table, int table_stride,
+                                int64_t num_pages, float* out, float* lse_ws, uint64_t ws_bytes,
+                                pa_stream_t stream) {
   Batch bt;
   Schedule sch;
-  const int st = rebuild_batch(plan, q_lens, hist_lens, &bt, &sch);
+  const int st = rebuild_batch(plan, nullptr, q_lens, hist_lens, &bt, &sch);
   if (st != PA_OK) return st;
+  return run_batch(plan, nullptr, bt, sch, q, k_pool, v_pool, block_table, table_stride,
+                   num_pages, out, lse_ws, ws_bytes, stream);
+}
+
+// The merge of a batch's cut row blocks into out (OUT: its type); nothing without any.
+template <int OUT>
+static int merge_batch(const pa_plan_t* plan, const Batch& bt, const Schedule& sch,
+                       const float* lse_ws, uint64_t ws_bytes, float* out, pa_stream_t stream) {
   if (sch.split.empty()) return PA_OK;
   if (!lse_ws || ws_bytes < plan->ws_bytes || !aligned16(lse_ws)) return PA_ERR_WORKSPACE;
   if (!out || !aligned16(out)) return PA_ERR_INVALID_ARG;
@@ -1602,12 +1786,43 @@ extern "C" int pa_batch_combine(const pa_plan_t* plan, const int32_t* q_lens,
   for (size_t i = 0; i < bt.seq.size(); ++i) table.seq[i] = bt.seq[i];
   const int D = plan->head_dim;
   const int64_t warps = (int64_t)sch.split.size() * sch.rows_per_block;
-  combine_blocks_kernel<<<(unsigned)((warps + 7) / 8), 256, 0,
-                          reinterpret_cast<cudaStream_t>(stream)>>>(
+  combine_blocks_kernel<OUT><<<(unsigned)((warps + 7) / 8), 256, 0,
+                               reinterpret_cast<cudaStream_t>(stream)>>>(
       lse_ws, lse_ws + (int64_t)sch.n_slots * sch.rows_per_block * D, out, table,
       (int)sch.split.size(), sch.rows_per_block, 0, plan->n_kv_heads, plan->group, 0,
       plan->n_q_heads, D, (int)bt.seq.size());
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+extern "C" int pa_batch_combine(const pa_plan_t* plan, const int32_t* q_lens,
+                                const int64_t* hist_lens, const float* lse_ws, uint64_t ws_bytes,
+                                float* out, pa_stream_t stream) {
+  Batch bt;
+  Schedule sch;
+  const int st = rebuild_batch(plan, nullptr, q_lens, hist_lens, &bt, &sch);
+  if (st != PA_OK) return st;
+  return merge_batch<kOutF32>(plan, bt, sch, lse_ws, ws_bytes, out, stream);
+}
+
+extern "C" int pa_window_prefill(const pa_plan_t* plan, const int32_t* q_lens,
+                                 const int64_t* hist_lens, int window, int n_sinks, const void* q,
+                                 const void* k_pool, const void* v_pool,
+                                 const int32_t* block_table, int table_stride, int64_t num_pages,
+                                 void* out, float* lse_ws, uint64_t ws_bytes,
+                                 pa_stream_t stream) {
+  if (window < 1 || n_sinks < 0) return PA_ERR_INVALID_ARG;
+  const Window win{window, n_sinks};
+  Batch bt;
+  Schedule sch;
+  int st = rebuild_batch(plan, &win, q_lens, hist_lens, &bt, &sch);
+  if (st != PA_OK) return st;
+  float* o = static_cast<float*>(out);
+  st = run_batch(plan, &win, bt, sch, q, k_pool, v_pool, block_table, table_stride, num_pages, o,
+                 lse_ws, ws_bytes, stream);
+  if (st != PA_OK) return st;
+  return plan->dtype == PA_BF16
+             ? merge_batch<kOutBf16>(plan, bt, sch, lse_ws, ws_bytes, o, stream)
+             : merge_batch<kOutF16>(plan, bt, sch, lse_ws, ws_bytes, o, stream);
 }
 
 // ---------------------------------------------------------------- entry point without allocation
@@ -1688,6 +1903,115 @@ extern "C" int pa_kv_publish(int n_kv_heads, int head_dim, int page_size, int dt
                       static_cast<const uint8_t*>(k_staged) + off,
                       static_cast<const uint8_t*>(v_staged) + off, k_pool, v_pool, page_table,
                       num_pages, first_pos, rows, stream);
+}
+
+extern "C" int pa_block_tables(int batch, const int32_t* q_lens, const int32_t* hist_lens,
+                               int page_size, int64_t num_pages, const int32_t* free_pages,
+                               int n_free, const int32_t* pages_used, int32_t* pages_used_out,
+                               int32_t* block_table, int table_stride, int max_rows,
+                               int32_t* slots, int32_t* positions, int32_t* cu_q_lens,
+                               int32_t* seq_lens, pa_stream_t stream) {
+  if (batch <= 0 || num_pages <= 0 || n_free < 0 || table_stride <= 0 || max_rows < 0)
+    return PA_ERR_INVALID_ARG;
+  if (!q_lens || !hist_lens || !pages_used || !pages_used_out || !block_table || !cu_q_lens ||
+      !seq_lens || (n_free > 0 && !free_pages) || (max_rows > 0 && (!slots || !positions)))
+    return PA_ERR_INVALID_ARG;
+  if (pages_used == pages_used_out) return PA_ERR_INVALID_ARG;  // other blocks still read it
+  if (page_size < 16 || page_size > 128 || (page_size & (page_size - 1))) return PA_ERR_UNSUPPORTED;
+  if (batch > kStepMaxSeqs || num_pages >= ((int64_t(1) << 31) - kTileKeys) / page_size)
+    return PA_ERR_UNSUPPORTED;
+  // Four rows a thread up to a block per SM: every block repeats the scan of the lengths.
+  const int64_t want = ((int64_t)max_rows + 4 * kStepThreads - 1) / (4 * kStepThreads);
+  const unsigned blocks = (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, 148));
+  block_tables_kernel<<<blocks, kStepThreads, 2 * (batch + 1) * sizeof(int32_t),
+                        reinterpret_cast<cudaStream_t>(stream)>>>(
+      batch, q_lens, hist_lens, __builtin_ctz((unsigned)page_size), (int32_t)num_pages, free_pages,
+      n_free, pages_used, pages_used_out, block_table, table_stride, max_rows, slots, positions,
+      cu_q_lens, seq_lens);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+namespace pa {
+template <int D, bool BF16, int NU>
+static void launch_qk_rope(unsigned blocks, cudaStream_t st, const RopeArgs& a, bool interleaved) {
+  if (interleaved)
+    qk_rope_append_kernel<D, BF16, true, NU><<<blocks, 256, 0, st>>>(a);
+  else
+    qk_rope_append_kernel<D, BF16, false, NU><<<blocks, 256, 0, st>>>(a);
+}
+template <int D, bool BF16>
+static int run_qk_rope(RopeArgs& a, bool interleaved, cudaStream_t st) {
+  constexpr int HPW = 256 / D;  // heads of a warp's set
+  constexpr int NU = 4;
+  a.q_warps = (a.Hq + NU * HPW - 1) / (NU * HPW);
+  a.kv_warps = (2 * a.Hkv + NU * HPW - 1) / (NU * HPW);
+  const int64_t blocks = ((int64_t)a.rows * (a.q_warps + a.kv_warps) + 7) / 8;
+  if (blocks >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
+  launch_qk_rope<D, BF16, NU>((unsigned)blocks, st, a, interleaved);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+}  // namespace pa
+
+extern "C" int pa_qk_rope_append(int n_q_heads, int n_kv_heads, int head_dim, int page_size,
+                                 int dtype, int rows, const void* q, int64_t q_stride,
+                                 const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                 const int32_t* positions, const int32_t* slots,
+                                 const float* rope, int rot_dim, int64_t max_pos, int interleaved,
+                                 const void* q_weight, const void* k_weight, int weight_f32,
+                                 float eps, void* q_out, void* k_pool, void* v_pool,
+                                 int64_t num_pages, pa_stream_t stream) {
+  if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_INVALID_ARG;
+  if (n_q_heads <= 0 || n_kv_heads <= 0 || rows < 0 || num_pages <= 0 || max_pos <= 0)
+    return PA_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || isinf(eps)) return PA_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return PA_ERR_UNSUPPORTED;
+  if (page_size < 16 || page_size > 128 || (page_size & (page_size - 1))) return PA_ERR_UNSUPPORTED;
+  if (rot_dim < 16 || rot_dim > head_dim || rot_dim % 16) return PA_ERR_UNSUPPORTED;
+  if (num_pages >= ((int64_t(1) << 31) - kTileKeys) / page_size) return PA_ERR_UNSUPPORTED;
+  if (rows == 0) return PA_OK;
+  if (!q || !k || !v || !positions || !slots || !rope || !q_out || !k_pool || !v_pool)
+    return PA_ERR_INVALID_ARG;
+  const int64_t qw = (int64_t)n_q_heads * head_dim, kw = (int64_t)n_kv_heads * head_dim;
+  if (q_stride < qw || k_stride < kw || v_stride < kw || q_stride % 8 || k_stride % 8 ||
+      v_stride % 8)
+    return PA_ERR_INVALID_ARG;
+  for (const void* p : {q, k, v, (const void*)rope, (const void*)q_out, (const void*)k_pool,
+                        (const void*)v_pool, q_weight, k_weight})
+    if (!aligned16(p)) return PA_ERR_INVALID_ARG;
+  RopeArgs a;
+  memset(&a, 0, sizeof a);
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.positions = positions;
+  a.slots = slots;
+  a.rope = rope;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_pool = static_cast<uint16_t*>(k_pool);
+  a.v_pool = static_cast<uint16_t*>(v_pool);
+  a.max_pos = max_pos;
+  a.n_slots = num_pages * page_size;
+  a.eps = eps;
+  a.rows = rows;
+  a.Hq = n_q_heads;
+  a.Hkv = n_kv_heads;
+  a.rot_dim = rot_dim;
+  a.weight_f32 = weight_f32;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool bf16 = dtype == PA_BF16;
+  switch (head_dim) {
+    case 64: return bf16 ? run_qk_rope<64, true>(a, interleaved, st)
+                         : run_qk_rope<64, false>(a, interleaved, st);
+    case 128: return bf16 ? run_qk_rope<128, true>(a, interleaved, st)
+                          : run_qk_rope<128, false>(a, interleaved, st);
+    default: return bf16 ? run_qk_rope<256, true>(a, interleaved, st)
+                         : run_qk_rope<256, false>(a, interleaved, st);
+  }
 }
 
 extern "C" int pa_device_error(int* flags, int reset) {

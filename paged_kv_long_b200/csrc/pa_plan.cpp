@@ -346,12 +346,12 @@ int batch_ctas_per_unit(int head_dim, int G, int batch, const int32_t* q_lens) {
 }
 
 bool build_batch(int num_sms, int head_dim, int per, int G, int Hkv, const Batch& bt,
-                 Schedule* out) {
+                 Schedule* out, const Window* win) {
   // One-row batches on the swapped decode kernel: two CTA slots per SM.
   if (batch_decode_swapped(head_dim, G, per, bt.seq.data(), (int)bt.seq.size()))
     num_sms *= kDecCtasPerSm;
   // one sequence: the single piece's schedule (row blocks numbered the same way)
-  if (bt.seq.size() == 1 && per == ctas_per_unit_for(head_dim))
+  if (!win && bt.seq.size() == 1 && per == ctas_per_unit_for(head_dim))
     return balanced_piece(q_tiles_for(bt.seq[0].rows, G), bt.seq[0].rows, bt.seq[0].hist, G,
                           Hkv, head_dim, num_sms, out);
   const int slots = std::max(1, num_sms / per);
@@ -363,31 +363,45 @@ bool build_batch(int num_sms, int head_dim, int per, int G, int Hkv, const Batch
       int64_t qu;
       int g;
       rb_coords((int32_t)local, q_units, Hkv, &qu, &g);
-      len.push_back(unit_kv_tiles(qu, per, q_tiles, sq.rows, G, sq.hist));
+      if (!win) {
+        len.push_back(unit_kv_tiles(qu, per, q_tiles, sq.rows, G, sq.hist));
+        continue;
+      }
+      const int64_t last = std::min(qu * per + per - 1, q_tiles - 1);
+      int64_t head, gap, n;
+      window_tiles(sq.hist + tile_first_token(qu * per, G),
+                   sq.hist + tile_last_token(last, sq.rows, G), win->window, win->sinks, &head,
+                   &gap, &n);
+      len.push_back(n);
     }
   }
   std::vector<int32_t> order(len.size());
   for (size_t i = 0; i < order.size(); ++i) order[i] = (int32_t)i;
   std::stable_sort(order.begin(), order.end(),
                    [&](int32_t x, int32_t y) { return len[x] > len[y]; });
-  if (wrap_around(len, order, slots, per, head_dim, out)) return true;
+  const bool cut = wrap_around(len, order, slots, per, head_dim, out);
+  if (cut && !win) return true;
   // Too many row blocks to also cut some (the item table holds 512): every row block whole,
-  // longest first, as the hardware's first-free dispatch then runs them (LPT order).
+  // longest first, as the hardware's first-free dispatch then runs them (LPT order). Windowed
+  // row blocks are short, so the parts' start-up and merge can cost more than the balance
+  // gains: there the cut schedule is taken only where its simulated time is the smaller.
   if (len.size() > (size_t)kMaxItems || len.empty()) return false;
   const CostModel cm(head_dim);
   Schedule sch;
   sch.rows_per_block = per * kTileRows;
   for (int32_t rb : order) sch.items.push_back(PaItem{rb, 0, (int32_t)len[rb], -1});
   sch.makespan_us = simulate_items(sch.items, slots, cm);
+  if (cut && out->makespan_us <= sch.makespan_us) return true;
   *out = std::move(sch);
   return true;
 }
 
 }  // namespace pa
 
-extern "C" int pa_batch_plan(int num_sms, int n_q_heads, int n_kv_heads, int head_dim,
-                             int page_size, int batch, const int32_t* q_lens,
-                             const int64_t* hist_lens, int dtype, float scale, pa_plan_t* plan) {
+// pa_batch_plan, and pa_window_plan with a window.
+static int plan_batch(int num_sms, int n_q_heads, int n_kv_heads, int head_dim, int page_size,
+                      int batch, const int32_t* q_lens, const int64_t* hist_lens,
+                      const pa::Window* win, int dtype, float scale, pa_plan_t* plan) {
   if (!plan) return PA_ERR_INVALID_ARG;
   memset(plan, 0, sizeof *plan);
   if (num_sms <= 0 || n_q_heads <= 0 || n_kv_heads <= 0) return PA_ERR_INVALID_ARG;
@@ -406,7 +420,7 @@ extern "C" int pa_batch_plan(int num_sms, int n_q_heads, int n_kv_heads, int hea
   const int st = pa::describe_batch(batch, q_lens, hist_lens, G, n_kv_heads, per, &bt);
   if (st != PA_OK) return st;
   pa::Schedule sch;
-  if (!pa::build_batch(num_sms, head_dim, per, G, n_kv_heads, bt, &sch))
+  if (!pa::build_batch(num_sms, head_dim, per, G, n_kv_heads, bt, &sch, win))
     return PA_ERR_UNSUPPORTED;
   int64_t q_tiles = 0;
   for (const pa::PaSeq& sq : bt.seq) q_tiles += pa::q_tiles_for(sq.rows, G);
@@ -421,7 +435,7 @@ extern "C" int pa_batch_plan(int num_sms, int n_q_heads, int n_kv_heads, int hea
   plan->splits = sch.max_parts;
   plan->paged = 1;
   plan->dtype = dtype;
-  plan->policy = PA_POLICY_BALANCED;
+  plan->policy = win ? PA_POLICY_WINDOW : PA_POLICY_BALANCED;
   plan->ctas_per_unit = per;
   plan->batch = batch;
   plan->hist_len = bt.max_hist;
@@ -429,6 +443,49 @@ extern "C" int pa_batch_plan(int num_sms, int n_q_heads, int n_kv_heads, int hea
   plan->scale = scale > 0.0f ? scale : (float)(1.0 / sqrt((double)head_dim));
   plan->est_us = (float)sch.makespan_us;
   plan->ws_bytes = (uint64_t)sch.n_slots * sch.rows_per_block * (head_dim + 1) * 4ull;
+  return PA_OK;
+}
+
+extern "C" int pa_batch_plan(int num_sms, int n_q_heads, int n_kv_heads, int head_dim,
+                             int page_size, int batch, const int32_t* q_lens,
+                             const int64_t* hist_lens, int dtype, float scale, pa_plan_t* plan) {
+  return plan_batch(num_sms, n_q_heads, n_kv_heads, head_dim, page_size, batch, q_lens, hist_lens,
+                    nullptr, dtype, scale, plan);
+}
+
+extern "C" int pa_window_plan(int num_sms, int n_q_heads, int n_kv_heads, int head_dim,
+                              int page_size, int batch, const int32_t* q_lens,
+                              const int64_t* hist_lens, int window, int n_sinks, int dtype,
+                              float scale, pa_plan_t* plan) {
+  if (!plan) return PA_ERR_INVALID_ARG;
+  memset(plan, 0, sizeof *plan);
+  if (window < 1 || n_sinks < 0) return PA_ERR_INVALID_ARG;
+  const pa::Window win{window, n_sinks};
+  return plan_batch(num_sms, n_q_heads, n_kv_heads, head_dim, page_size, batch, q_lens, hist_lens,
+                    &win, dtype, scale, plan);
+}
+
+extern "C" int pa_window_decode_plan(int num_sms, int n_q_heads, int n_kv_heads, int head_dim,
+                                     int page_size, int batch, int64_t max_seq_len, int window,
+                                     int n_sinks, int dtype, float scale, int splits_override,
+                                     pa_plan_t* plan) {
+  if (!plan) return PA_ERR_INVALID_ARG;
+  memset(plan, 0, sizeof *plan);
+  if (window < 1 || n_sinks < 0 || max_seq_len < 1) return PA_ERR_INVALID_ARG;
+  // the most tiles a sequence's window and sinks reach, whatever its length up to max_seq_len
+  const int64_t tiles =
+      std::min(pa::ceil_div64(max_seq_len, pa::kTileKeys),
+               pa::ceil_div64(n_sinks, pa::kTileKeys) + pa::ceil_div64(window - 1, pa::kTileKeys) +
+                   1);
+  const int st = pa_decode_plan(num_sms, n_q_heads, n_kv_heads, head_dim, page_size, batch,
+                                tiles * pa::kTileKeys, dtype, scale, splits_override, plan);
+  if (st != PA_OK) return st;
+  if (max_seq_len + pa::kTileKeys >= (int64_t(1) << 31)) {
+    memset(plan, 0, sizeof *plan);
+    return PA_ERR_UNSUPPORTED;
+  }
+  plan->policy = PA_POLICY_WINDOW_DECODE;
+  plan->hist_len = max_seq_len;
   return PA_OK;
 }
 
@@ -611,19 +668,35 @@ static int write_items(const pa::Schedule& sch, int32_t* items, int cap) {
   return n;
 }
 
-extern "C" int pa_batch_schedule_items(const pa_plan_t* plan, const int32_t* q_lens,
-                                       const int64_t* hist_lens, int32_t* items, int cap) {
-  if (!plan || plan->batch <= 0 || plan->policy != PA_POLICY_BALANCED) return PA_ERR_INVALID_ARG;
+// The items of a batch plan, or with a window of a window plan.
+static int batch_items(const pa_plan_t* plan, const int32_t* q_lens, const int64_t* hist_lens,
+                       const pa::Window* win, int32_t* items, int cap) {
+  if (!plan || plan->batch <= 0 ||
+      plan->policy != (win ? PA_POLICY_WINDOW : PA_POLICY_BALANCED))
+    return PA_ERR_INVALID_ARG;
   pa::Batch bt;
   const int st = pa::describe_batch(plan->batch, q_lens, hist_lens, plan->group,
                                     plan->n_kv_heads, plan->ctas_per_unit, &bt);
   if (st != PA_OK) return st;
   pa::Schedule sch;
   if (!pa::build_batch(plan->num_sms, plan->head_dim, plan->ctas_per_unit, plan->group,
-                       plan->n_kv_heads, bt, &sch) ||
+                       plan->n_kv_heads, bt, &sch, win) ||
       (int64_t)sch.items.size() != plan->units)
     return PA_ERR_INVALID_ARG;
   return write_items(sch, items, cap);
+}
+
+extern "C" int pa_batch_schedule_items(const pa_plan_t* plan, const int32_t* q_lens,
+                                       const int64_t* hist_lens, int32_t* items, int cap) {
+  return batch_items(plan, q_lens, hist_lens, nullptr, items, cap);
+}
+
+extern "C" int pa_window_schedule_items(const pa_plan_t* plan, const int32_t* q_lens,
+                                        const int64_t* hist_lens, int window, int n_sinks,
+                                        int32_t* items, int cap) {
+  if (window < 1 || n_sinks < 0) return PA_ERR_INVALID_ARG;
+  const pa::Window win{window, n_sinks};
+  return batch_items(plan, q_lens, hist_lens, &win, items, cap);
 }
 
 extern "C" int pa_schedule_items(const pa_plan_t* plan, int32_t* items, int cap) {

@@ -92,7 +92,7 @@ struct PairSync {
 
 // Softmax + epilogue warps of the pair kernel (warps 0-3, one thread per packed Q row of this
 // CTA's tile = tensor-memory lane).
-template <bool PAGED, bool BF16, class VTail>
+template <bool PAGED, bool BF16, bool WIN, class VTail>
 __device__ __forceinline__ void softmax_pair_role(const PrefillArgs& a, const SoftmaxCtx& x,
                                                   const PairSync& y, VTail&& v_tail) {
   constexpr int D = 256;
@@ -147,7 +147,7 @@ __device__ __forceinline__ void softmax_pair_role(const PrefillArgs& a, const So
                      tmo);
   };
   for (int j = 0; j < n; ++j) {
-    const int64_t key0 = (kt0 + j) * kTileKeys;
+    const int64_t key0 = kv_tile<WIN>(a, kt0 + j) * kTileKeys;
     if (!warp_wait(x.bar_sfull, (uint32_t)j & 1u, abort_flag, tmo)) {
       ok = false;
       break;
@@ -176,6 +176,7 @@ __device__ __forceinline__ void softmax_pair_role(const PrefillArgs& a, const So
       for (int c = 0; c < kTileKeys; ++c)
         if (c > rel) sv[c] = -INFINITY;
     }
+    if constexpr (WIN) mask_window(a, limit, key0, sv);
     // row max: eight independent chains, then a tree
     float mx8[8];
 #pragma unroll
@@ -229,10 +230,10 @@ __device__ __forceinline__ void softmax_pair_role(const PrefillArgs& a, const So
       break;
     }
 
-    // The sequence's last tile, partly past its end (paged pools): this CTA's half of the V
-    // rows past the end is zeroed in shared memory before PV reads it.
-    const bool tail = PAGED && key0 + kTileKeys > a.total_keys;
-    if (tail && !v_tail(j, key0 + r >= a.total_keys ? r : -1)) {
+    // The sequence's last tile, partly past its end (paged pools), or a tile with keys outside
+    // every window: this CTA's half of those V rows is zeroed in shared memory before PV reads it.
+    const bool tail = PAGED && tile_unseen<WIN>(a, key0);
+    if (tail && !v_tail(j, key_unseen<WIN>(a, key0 + r) ? r : -1)) {
       ok = false;
       break;
     }
@@ -262,11 +263,11 @@ __device__ __forceinline__ void softmax_pair_role(const PrefillArgs& a, const So
   if (ok) ok = wait_pv(n - 1);
   if (ok) {
     tc_fence_after();
-    write_row<D>(a, x, r, valid, tok, head, m_run, l_run, t_lane);
+    write_row<D, WIN, BF16>(a, x, r, valid, tok, head, m_run, l_run, t_lane);
   }
 }
 
-template <bool PAGED, bool BF16>
+template <bool PAGED, bool BF16, bool WIN>
 __global__ void __launch_bounds__(kPairThreads, 1)
     prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v,
@@ -286,12 +287,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   int g, s, slot = kSlotUniform;
   if (a.balanced) {
     const PaItem it = items.item[blockIdx.x >> 1];
-    const int32_t rb = a.batch > 0 ? batch_rebase<D>(a, items, it.rb) : it.rb;
+    const int32_t rb = a.batch > 0 ? batch_rebase<D, WIN>(a, items, it.rb) : it.rb;
     rb_coords(rb, (a.q_tiles + 1) / 2, a.Hkv, &tp, &g);
     s = 0;
     kt0 = it.kt0;
     kt1 = it.kt1;
     slot = it.slot;
+    if constexpr (WIN) {  // the pair's rows: both CTAs walk the same tiles
+      const int64_t last = 2 * tp + 1 < a.q_tiles ? 2 * tp + 1 : a.q_tiles - 1;
+      set_window(a, a.hist_len + tile_first_token(2 * tp, a.G),
+                 a.hist_len + tile_last_token(last, a.R, a.G));
+    }
   } else {
     unit_coords(blockIdx.x >> 1, (a.q_tiles + 1) / 2, a.Hkv, a.splits, &tp, &g, &s);
     const int64_t qt_last = 2 * tp + 1 < a.q_tiles ? 2 * tp + 1 : a.q_tiles - 1;
@@ -320,8 +326,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   int32_t pre_row0 = a.oob_row, pre_row1 = a.oob_row;
   if (warp > kMmaWarp && warp < kPairPvWarp) {
     const bool report = warp == kMmaWarp + 1;
-    pre_row0 = tile_page_row<PAGED>(a, kt0, n, 0, lane, report);
-    pre_row1 = tile_page_row<PAGED>(a, kt0, n, 1, lane, report);
+    pre_row0 = tile_page_row<PAGED, WIN>(a, kt0, n, 0, lane, report);
+    pre_row1 = tile_page_row<PAGED, WIN>(a, kt0, n, 1, lane, report);
   }
   auto bar = [&](int i) -> uint32_t { return sb + C::BAR_OFF + 8u * (uint32_t)i; };
   auto slot_addr = [&](uint32_t slot) -> uint32_t { return sb + C::RING_OFF + slot * kPanel; };
@@ -329,10 +335,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF + 4);
   const uint32_t leader_bar0 = mapa_shared(sb + C::BAR_OFF, 0);  // rank 0's barriers
   auto leader_bar = [&](int i) -> uint32_t { return leader_bar0 + 8u * (uint32_t)i; };
-  // The sequence's last KV tile, partly past the end (paged pools only: there the rows after
-  // the last key hold another sequence's data or nothing), is the unit's last tile; its V
-  // fills are the V ring's last two (2n-2, 2n-1).
-  const bool has_tail = PAGED && (kt0 + n) * kTileKeys > a.total_keys;
+  // Tail tiles: the sequence's last KV tile, partly past the end (paged pools only: there the
+  // rows after the last key hold another sequence's data or nothing), is the unit's last tile;
+  // its V fills are the V ring's last two (2n-2, 2n-1). With a window also the tiles that hold
+  // keys between the sinks and the window (up to two more, anywhere in the unit).
+  auto tail_tile = [&](int j) -> bool {
+    return PAGED && tile_unseen<WIN>(a, kv_tile<WIN>(a, kt0 + j) * kTileKeys);
+  };
+  const bool has_tail = tail_tile(n - 1);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NSLOT; ++i) {
@@ -414,13 +424,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // Keys past the sequence in its last page hold arbitrary bits; P is 0 there but 0 * NaN
     // is NaN inside the MMA, so this CTA's half of those V rows is zeroed before PV.
     // Those fills complete on this CTA's own barrier: on rank 1 that barrier sees no other
-    // phase, so its parity is 0.
+    // phase, so its parity is 0 (with a window: the count of earlier tail tiles on the same
+    // slots, those of the same tile parity). Every earlier fill of the slots has landed by then:
+    // PV(j-2) has read the last one.
+    uint32_t n_tails[2] = {0, 0};
     auto v_tail = [&](int j, int r) -> bool {
       const uint32_t seq0 = 2u * (uint32_t)j;
+      const uint32_t phase1 = WIN ? n_tails[j & 1]++ & 1u : 0u;
       bool okv = true;
       for (int k = 0; k < 2 && okv; ++k)
         okv = warp_wait(bar(C::B_FULL + pair_v_slot(seq0 + k)),
-                        rank == 0 ? pair_v_phase(seq0 + k) : 0u, abort_flag, tmo);
+                        rank == 0 ? pair_v_phase(seq0 + k) : phase1, abort_flag, tmo);
       if (!okv || r < 0) return okv;
       for (int pl = 0; pl < 2; ++pl) {
         const uint32_t off = v_offset_pair((uint32_t)r, pl, a.v_shift);
@@ -430,7 +444,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
       return true;
     };
-    softmax_pair_role<PAGED, BF16>(a, sc, ps, v_tail);
+    softmax_pair_role<PAGED, BF16, WIN>(a, sc, ps, v_tail);
   } else if (warp > kMmaWarp && warp < kPairPvWarp) {
     // ============================================================ TMA issuers (two warps)
     // Warp 5 fills the K ring (K(0), K(1), ... in tile order), warp 6 the V ring; lanes issue
@@ -446,8 +460,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     auto fetch = [&](int jt) -> int32_t {
       int32_t row = a.oob_row;
       if constexpr (PAGED) {
-        const int64_t lp = (kt0 + jt) * ppt + lane;
-        if (jt < n && lane < ppt && lp < a.table_len) {
+        const int64_t lp = kv_tile<WIN>(a, kt0 + jt) * ppt + lane;
+        if (jt < n && lane < ppt && lp < a.table_len && page_seen<WIN>(a, lp)) {
           const int32_t e = __ldg(a.page_table + lp);
           if (e >= 0 && e < a.num_pages)
             row = e << a.page_shift;
@@ -514,13 +528,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
     };
     // V half tile j (dims 128*rank..+127 of tile j): slot k holds keys 64k..64k+63
+    uint32_t v_tails[4] = {0, 0, 0, 0};  // tail fills issued into each V slot
     auto issue_v = [&](int j, int32_t rows) {
-      const bool tail = has_tail && j == n - 1;
+      const bool tail = WIN ? tail_tile(j) : has_tail && j == n - 1;
       for (int k = 0; k < 2 && ok; ++k) {
         const uint32_t q = 2u * (uint32_t)j + (uint32_t)k;
         const int32_t row = key_row(rows, 64 * k + lane * v_rows);
         const uint32_t sl = pair_v_slot(q);
         if (!(ok = acquire(sl, q / C::VSLOT, tail))) break;
+        if (WIN && tail) ++v_tails[2 * (j & 1) + k];
         if (lane < v_per_slot) {
           const uint32_t dst = slot_addr(sl) + lane * (v_rows * 256);
           if (rank == 0 || tail)
@@ -561,8 +577,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // so rank 1's copies have landed as well; rank 1 drains only the tail fills on its own
     // barrier, and it stays resident until rank 0 has finished (teardown handshake below).
     const uint32_t ring = w == 0 ? C::KSLOT : C::VSLOT;
+    if (WIN && w == 1 && rank == 1) {  // each slot's last tail fill, on this CTA's barriers
+      for (uint32_t k = 0; k < 4; ++k)
+        if (v_tails[k] > 0)
+          drain_wait(bar(C::B_FULL + pair_v_slot(k)), (v_tails[k] - 1) & 1u, abort_flag, tmo);
+    }
     for (uint32_t q = issued > ring ? issued - ring : 0; q < issued; ++q) {
-      const bool tail = w == 1 && has_tail && q + 2u >= 2u * (uint32_t)n;
+      const bool tail = !WIN && w == 1 && has_tail && q + 2u >= 2u * (uint32_t)n;
       if (rank == 0 || tail)
         drain_wait(bar(C::B_FULL + (w == 0 ? pair_k_slot(q) : pair_v_slot(q))),
                    rank == 0 ? (w == 0 ? pair_k_phase(q) : pair_v_phase(q)) : 0u, abort_flag,
