@@ -67,9 +67,11 @@ typedef enum {
    * schedule would not fit the kernel's tables (512 items, 256 cut row blocks, 32 parts);
    * the plan's `policy` field says which was used. */
   PA_POLICY_BALANCED = 3,
-  /* Read only, in the plans of pa_window_plan and pa_window_decode_plan (pa_plan takes neither). */
+  /* Read only, in the plans of pa_window_plan, pa_window_decode_plan and
+   * pa_prefix_decode_plan (pa_plan takes none of them). */
   PA_POLICY_WINDOW = 4,
-  PA_POLICY_WINDOW_DECODE = 5
+  PA_POLICY_WINDOW_DECODE = 5,
+  PA_POLICY_PREFIX_DECODE = 6
 } pa_policy;
 
 /* Rows of the packed (token, head) Q tile, and keys per KV tile, of the kernel. */
@@ -319,17 +321,49 @@ int pa_window_schedule_items(const pa_plan_t* plan, const int32_t* q_lens,
 
 /*
  * pa_window_decode_plan / pa_window_decode — one query token per sequence, lengths on the device:
- * arguments, limits and layouts of pa_decode_plan and pa_decode, with the window, the sinks and
- * the output's type; the S splits share a sequence's visible KV tiles. pa_window_decode also
- * merges the splits. A sequence with no key (a padded row) gets zeros. The plan's policy is
- * PA_POLICY_WINDOW_DECODE and its hist_len max_seq_len; `window` and `n_sinks` must be those it
- * was made with (a larger window gives right results too, in longer units).
+ * arguments, limits and layouts of pa_decode, with the window, the sinks and the output's type. A
+ * sequence with no key (a padded row) gets zeros. pa_window_decode also merges what it split.
+ * Groups of up to 8 heads at head dim 128 or 256 run on CTAs that stay for the step (plan->units
+ * of them, two per SM), each streaming an equal share of all sequences' visible KV tiles, whatever
+ * the lengths on the device are; the others in uniform splits (plan->splits). The plan's policy is
+ * PA_POLICY_WINDOW_DECODE and its hist_len max_seq_len, which only sizes the launch: longer
+ * sequences are right too. `window` and `n_sinks` must be those it was made with.
  */
 int pa_window_decode_plan(int num_sms, int n_q_heads, int n_kv_heads, int head_dim, int page_size,
                           int batch, int64_t max_seq_len, int window, int n_sinks, int dtype,
-                          float scale, int splits_override, pa_plan_t* plan);
+                          float scale, pa_plan_t* plan);
 int pa_window_decode(const pa_plan_t* plan, int window, int n_sinks, const void* q,
                      const void* k_pool, const void* v_pool, const int32_t* block_table,
+                     int table_stride, const int32_t* seq_lens, int64_t num_pages, void* out,
+                     float* lse_ws, uint64_t ws_bytes, pa_stream_t stream);
+
+/*
+ * pa_prefix_decode_plan / pa_prefix_decode — a decode step (one query token per sequence, lengths
+ * on the device, pa_decode's arguments and limits) whose sequences share their first prefix_len
+ * keys, as requests on one long prompt do: the shared keys are read and multiplied once for the
+ * whole batch, packed 128 (sequence, head) rows to a tile, each sequence's own keys as in
+ * pa_decode, and the parts merged by their log-sum-exps. The result is that of pa_decode on the
+ * same sequences, rounded once to the type of q.
+ *   prefix_len    keys shared: a multiple of the page size, > 0 (pages are shared whole).
+ *   max_seq_len   of whole sequences, prefix included; it only sizes the launch of the own part:
+ *                 longer sequences are right too.
+ *   prefix_table  device int32 [prefix_len / PS]: the shared pages.
+ *   block_table   device int32 [batch][table_stride]: whole sequences, as for pa_decode; the
+ *                 entries of the first prefix_len / PS pages are not read.
+ *   seq_lens      device int32 [batch]: keys of each whole sequence. A sequence of at most
+ *                 prefix_len keys sees its first seq_lens[b] shared ones; one with no key (a
+ *                 padded row) gets zeros.
+ *   out           device [batch][Hq][D] of dtype.
+ *   lse_ws        workspace of plan->ws_bytes. The call merges its partials itself.
+ * The plan's policy is PA_POLICY_PREFIX_DECODE, splits the prefix's splits, units those of the own
+ * part; other entry points refuse it, and a prefix_len that needs another launch or workspace than
+ * the one it was made with is refused.
+ */
+int pa_prefix_decode_plan(int num_sms, int n_q_heads, int n_kv_heads, int head_dim, int page_size,
+                          int batch, int64_t prefix_len, int64_t max_seq_len, int dtype,
+                          float scale, pa_plan_t* plan);
+int pa_prefix_decode(const pa_plan_t* plan, int64_t prefix_len, const void* q, const void* k_pool,
+                     const void* v_pool, const int32_t* prefix_table, const int32_t* block_table,
                      int table_stride, const int32_t* seq_lens, int64_t num_pages, void* out,
                      float* lse_ws, uint64_t ws_bytes, pa_stream_t stream);
 

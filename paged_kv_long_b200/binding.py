@@ -27,7 +27,8 @@ EXPORTED = ("pa_plan", "pa_prefill", "pa_combine", "pa_prefill_noalloc", "pa_dev
             "pa_decode_plan", "pa_decode", "pa_batch_plan", "pa_batch_prefill",
             "pa_batch_combine", "pa_batch_schedule_items", "pa_kv_publish",
             "pa_window_plan", "pa_window_prefill", "pa_window_schedule_items",
-            "pa_window_decode_plan", "pa_window_decode", "pa_block_tables", "pa_qk_rope_append")
+            "pa_window_decode_plan", "pa_window_decode", "pa_prefix_decode_plan", "pa_prefix_decode",
+            "pa_block_tables", "pa_qk_rope_append")
 
 
 class PaError(RuntimeError):
@@ -124,11 +125,17 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
                                              ctypes.POINTER(ctypes.c_int32), i32]
     lib.pa_window_schedule_items.restype = i32
     lib.pa_window_decode_plan.argtypes = [i32, i32, i32, i32, i32, i32, i64, i32, i32, i32,
-                                          ctypes.c_float, i32, ctypes.POINTER(Plan)]
+                                          ctypes.c_float, ctypes.POINTER(Plan)]
     lib.pa_window_decode_plan.restype = i32
     lib.pa_window_decode.argtypes = [ctypes.POINTER(Plan), i32, i32, vp, vp, vp, vp, i32, vp, i64,
                                      vp, vp, u64, vp]
     lib.pa_window_decode.restype = i32
+    lib.pa_prefix_decode_plan.argtypes = [i32, i32, i32, i32, i32, i32, i64, i64, i32,
+                                          ctypes.c_float, ctypes.POINTER(Plan)]
+    lib.pa_prefix_decode_plan.restype = i32
+    lib.pa_prefix_decode.argtypes = [ctypes.POINTER(Plan), i64, vp, vp, vp, vp, vp, i32, vp, i64,
+                                     vp, vp, u64, vp]
+    lib.pa_prefix_decode.restype = i32
     lib.pa_block_tables.argtypes = [i32, vp, vp, i32, i64, vp, i32, vp, vp, vp, i32, i32, vp, vp,
                                     vp, vp, vp]
     lib.pa_block_tables.restype = i32
@@ -559,37 +566,56 @@ def window_schedule_items(wp: WindowPlan):
 
 def window_decode_plan(n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, batch: int,
                        max_seq_len: int, window: int, n_sinks: int = 0, dtype="bf16",
-                       scale: float = 0.0, splits: int = 0,
-                       num_sms: int | None = None) -> WindowPlan:
-    """pa_window_decode_plan: split count and workspace of a decode step under a sliding window
-    with sinks (host only)."""
+                       scale: float = 0.0, num_sms: int | None = None) -> WindowPlan:
+    """pa_window_decode_plan: launch and workspace of a decode step under a sliding window with
+    sinks (host only)."""
     window, n_sinks = _window_args(window, n_sinks)
     p = Plan()
     st = load_library().pa_window_decode_plan(num_sms or _num_sms(), n_q_heads, n_kv_heads,
                                               head_dim, page_size, batch, max_seq_len, window,
-                                              n_sinks, _dtype_code(dtype), scale, splits,
+                                              n_sinks, _dtype_code(dtype), scale,
                                               ctypes.byref(p))
     _check(st, "pa_window_decode_plan")
     return WindowPlan(p, window, n_sinks)
 
 
-def _same_device(first, *rest):
-    """All tensors (None skipped) sit on one CUDA device; returns it."""
-    for t in rest:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}: one device is needed")
-    return first.device
+# The calls below run once a layer and step, so their own cost counts: at a decode step's sizes
+# the kernels take 3-8 microseconds. A tensor's checks are four attribute reads (the messages come
+# from _require_cuda, on failure only), and the stream is read without building a Stream object.
 
 
-def _call(device, stream, fn, name, *args):
+def _require(t, name, dtype, shape, device):
+    """t is a contiguous CUDA tensor of this dtype, shape (None: any) and device index."""
+    try:
+        if (t.dtype is dtype and t.get_device() == device and t.is_contiguous()
+                and (shape is None or t.shape == shape)):
+            return
+    except AttributeError:
+        pass
+    _require_cuda(t, name, dtype, shape)
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, not on cuda:{device}: one device is "
+                     "needed")
+
+
+def _device_of(t, name) -> int:
+    """Index of the CUDA device that t (and so the call) is on."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _call(device: int, stream, fn, name, *args):
     """fn(*args, stream) with `device` current, on its current stream unless one is given."""
     import torch
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, _stream_ptr(stream))
+    ptr = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if device == torch._C._cuda_getDevice():
+        st = fn(*args, ptr)
     else:
         with torch.cuda.device(device):
-            st = fn(*args, _stream_ptr(stream))
-    _check(st, name)
+            st = fn(*args, ptr)
+    if st != 0:
+        raise PaError(st, name)
 
 
 def _used_on(stream, *tensors):
@@ -600,34 +626,34 @@ def _used_on(stream, *tensors):
             t.record_stream(stream)
 
 
-def _window_tensors(p: Plan, rows, q, k_pool, v_pool, block_table, out, ws, stream):
-    """Checks of the tensors that both window calls take; (out, ws, ws pointer, ws bytes)."""
+def _step_tensors(p: Plan, rows, q, k_pool, v_pool, block_table, out, ws, stream, device):
+    """Checks of the tensors that the window and prefix calls take; (out, ws, its pointer, its bytes)."""
     import torch
     dt = _torch_dtype(p)
-    Hq, Hkv, D, PS = p.n_q_heads, p.n_kv_heads, p.head_dim, p.page_size
-    _require_cuda(q, "q", dt, (rows, Hq, D))
-    _require_cuda(k_pool, "k_pool", dt)
-    _require_cuda(v_pool, "v_pool", dt, k_pool.shape)
-    if k_pool.dim() != 4 or k_pool.shape[1:] != (PS, Hkv, D):
+    D = p.head_dim
+    heads = (rows, p.n_q_heads, D)
+    _require(q, "q", dt, heads, device)
+    _require(k_pool, "k_pool", dt, None, device)
+    pool = k_pool.shape
+    if len(pool) != 4 or pool[1:] != (p.page_size, p.n_kv_heads, D):
         raise ValueError("k_pool must be [num_pages, page_size, Hkv, D]")
-    _require_cuda(block_table, "block_table", torch.int32)
+    _require(v_pool, "v_pool", dt, pool, device)
+    _require(block_table, "block_table", torch.int32, None, device)
     if block_table.dim() != 2 or block_table.shape[0] != p.batch:
         raise ValueError("block_table must be [batch, max_pages]")
     if out is None:
         out = torch.empty_like(q)
         _used_on(stream, out)
     else:
-        _require_cuda(out, "out", dt, (rows, Hq, D))
-    ws_ptr, ws_bytes = None, 0
-    if p.ws_bytes > 0:
-        if ws is None:
-            ws = workspace(p, q.device)
-            _used_on(stream, ws)
-        else:
-            _require_cuda(ws, "ws", torch.float32)
-        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel() * 4
-    _same_device(q, k_pool, v_pool, block_table, out, ws)
-    return out, ws, ws_ptr, ws_bytes
+        _require(out, "out", dt, heads, device)
+    if p.ws_bytes == 0:
+        return out, None, None, 0
+    if ws is None:
+        ws = torch.empty(p.ws_bytes // 4, dtype=torch.float32, device=q.device)
+        _used_on(stream, ws)
+    else:
+        _require(ws, "ws", torch.float32, None, device)
+    return out, ws, ws.data_ptr(), ws.numel() * 4
 
 
 def window_decode(wp: WindowPlan, q, k_pool, v_pool, block_table, seq_lens, out=None, ws=None,
@@ -639,10 +665,11 @@ def window_decode(wp: WindowPlan, q, k_pool, v_pool, block_table, seq_lens, out=
     p = wp.plan
     if wp.q_lens is not None:
         raise ValueError("a plan of window_plan runs with window_prefill")
-    _require_cuda(seq_lens, "seq_lens", torch.int32, (p.batch,))
-    out, ws, ws_ptr, ws_bytes = _window_tensors(p, p.batch, q, k_pool, v_pool, block_table, out,
-                                                ws, stream)
-    _call(_same_device(q, seq_lens), stream, load_library().pa_window_decode, "pa_window_decode",
+    device = _device_of(q, "q")
+    _require(seq_lens, "seq_lens", torch.int32, (p.batch,), device)
+    out, ws, ws_ptr, ws_bytes = _step_tensors(p, p.batch, q, k_pool, v_pool, block_table, out,
+                                                ws, stream, device)
+    _call(device, stream, load_library().pa_window_decode, "pa_window_decode",
           ctypes.byref(p), wp.window, wp.n_sinks, q.data_ptr(), k_pool.data_ptr(),
           v_pool.data_ptr(), block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(),
           k_pool.shape[0], out.data_ptr(), ws_ptr, ws_bytes)
@@ -656,12 +683,54 @@ def window_prefill(wp: WindowPlan, q, k_pool, v_pool, block_table, out=None, ws=
     p = wp.plan
     if wp.q_lens is None:
         raise ValueError("a plan of window_decode_plan runs with window_decode")
-    out, ws, ws_ptr, ws_bytes = _window_tensors(p, p.chunk_rows, q, k_pool, v_pool, block_table,
-                                                out, ws, stream)
-    _call(q.device, stream, load_library().pa_window_prefill, "pa_window_prefill",
+    device = _device_of(q, "q")
+    out, ws, ws_ptr, ws_bytes = _step_tensors(p, p.chunk_rows, q, k_pool, v_pool, block_table,
+                                                out, ws, stream, device)
+    _call(device, stream, load_library().pa_window_prefill, "pa_window_prefill",
           ctypes.byref(p), wp.q_lens.ctypes.data, wp.hist_lens.ctypes.data, wp.window, wp.n_sinks,
           q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(),
           block_table.shape[1], k_pool.shape[0], out.data_ptr(), ws_ptr, ws_bytes)
+    return out
+
+
+class PrefixPlan:
+    """A plan of pa_prefix_decode_plan with its prefix length."""
+
+    def __init__(self, plan: Plan, prefix_len: int):
+        self.plan = plan
+        self.prefix_len = prefix_len
+
+
+def prefix_decode_plan(n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, batch: int,
+                       prefix_len: int, max_seq_len: int, dtype="bf16", scale: float = 0.0,
+                       num_sms: int | None = None) -> PrefixPlan:
+    """pa_prefix_decode_plan: launch and workspace of a decode step over a shared prefix (host
+    only)."""
+    p = Plan()
+    st = load_library().pa_prefix_decode_plan(num_sms or _num_sms(), n_q_heads, n_kv_heads,
+                                              head_dim, page_size, batch, prefix_len, max_seq_len,
+                                              _dtype_code(dtype), scale, ctypes.byref(p))
+    _check(st, "pa_prefix_decode_plan")
+    return PrefixPlan(p, prefix_len)
+
+
+def prefix_decode(pp: PrefixPlan, q, k_pool, v_pool, prefix_table, block_table, seq_lens, out=None,
+                  ws=None, stream=None):
+    """pa_prefix_decode: one query token per sequence, the first prefix_len keys shared by all and
+    computed once (see include/pa.h). q [B, Hq, D]; prefix_table int32 [prefix_len / PS];
+    block_table int32 [B, max_pages] and seq_lens int32 [B] of whole sequences. Returns out
+    [B, Hq, D] of q's type."""
+    import torch
+    p = pp.plan
+    device = _device_of(q, "q")
+    _require(prefix_table, "prefix_table", torch.int32, (pp.prefix_len // p.page_size,), device)
+    _require(seq_lens, "seq_lens", torch.int32, (p.batch,), device)
+    out, ws, ws_ptr, ws_bytes = _step_tensors(p, p.batch, q, k_pool, v_pool, block_table, out,
+                                                ws, stream, device)
+    _call(device, stream, load_library().pa_prefix_decode, "pa_prefix_decode",
+          ctypes.byref(p), pp.prefix_len, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+          prefix_table.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+          seq_lens.data_ptr(), k_pool.shape[0], out.data_ptr(), ws_ptr, ws_bytes)
     return out
 
 
@@ -679,32 +748,28 @@ def block_tables(q_lens, hist_lens, free_pages, pages_used, block_table, max_row
     pages_used [1]), in the tensors of `out` when given (its pages_used not the input's)."""
     import torch
     i32 = torch.int32
-    _require_cuda(q_lens, "q_lens", i32)
+    device = _device_of(q_lens, "q_lens")
+    _require(q_lens, "q_lens", i32, None, device)
     if q_lens.dim() != 1:
         raise ValueError("q_lens must be [batch]")
     B = q_lens.shape[0]
-    _require_cuda(hist_lens, "hist_lens", i32, (B,))
-    _require_cuda(free_pages, "free_pages", i32)
+    _require(hist_lens, "hist_lens", i32, (B,), device)
+    _require(free_pages, "free_pages", i32, None, device)
     if free_pages.dim() != 1:
         raise ValueError("free_pages must be 1-D")
-    _require_cuda(pages_used, "pages_used", i32, (1,))
-    _require_cuda(block_table, "block_table", i32)
+    _require(pages_used, "pages_used", i32, (1,), device)
+    _require(block_table, "block_table", i32, None, device)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [batch, max_pages]")
     sizes = (max_rows, max_rows, B + 1, B, 1)
-    if out is None:  # one allocation, cut at multiples of four words
-        starts, total = [], 0
-        for n in sizes:
-            starts.append(total)
-            total += (n + 3) & ~3
-        buf = torch.empty(total, dtype=i32, device=q_lens.device)
+    if out is None:  # one allocation for all five
+        buf = torch.empty(2 * max_rows + 2 * B + 2, dtype=i32, device=q_lens.device)
         _used_on(stream, buf)
-        out = StepTables(*(buf[a:a + n] for a, n in zip(starts, sizes)))
+        out = StepTables._make(buf.split_with_sizes(sizes))
     else:
-        out = StepTables(*out)
+        out = StepTables._make(out)
         for t, name, n in zip(out, StepTables._fields, sizes):
-            _require_cuda(t, name, i32, (n,))
-    device = _same_device(q_lens, hist_lens, free_pages, pages_used, block_table, *out)
+            _require(t, name, i32, (n,), device)
     _call(device, stream, load_library().pa_block_tables, "pa_block_tables", B, q_lens.data_ptr(),
           hist_lens.data_ptr(), page_size, num_pages, free_pages.data_ptr(), free_pages.shape[0],
           pages_used.data_ptr(), out.pages_used.data_ptr(), block_table.data_ptr(),
@@ -723,22 +788,25 @@ def rope_table(max_pos: int, rot_dim: int, theta: float = 10000.0, device="cuda"
     return torch.cat([angle.cos(), angle.sin()], dim=1).float()
 
 
-def _require_rows(t, name, dtype, shape):
-    """t is [rows, H, D] on CUDA with contiguous rows; returns its row stride in elements."""
+def _require_rows(t, name, dtype, shape, device):
+    """t is [rows, H, D] on the device with contiguous rows; returns its row stride in elements."""
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    width = shape[1] * shape[2]
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, not on cuda:{device}: one device "
+                         "is needed")
+    rows, heads, D = shape
     s0, s1, s2 = t.stride()
-    if (s1 != shape[2] and shape[1] > 1) or s2 != 1:
+    if (s1 != D and heads > 1) or s2 != 1:
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    if shape[0] <= 1:
-        return width
-    if s0 < width or s0 % 8:
+    if rows <= 1:
+        return heads * D
+    if s0 < heads * D or s0 % 8:
         raise ValueError(f"the row stride of {name} must be a multiple of 8 and cover the row")
     return s0
 
@@ -751,44 +819,48 @@ def qk_rope_append(q, k, v, positions, slots, rope, k_pool, v_pool, q_weight=Non
     row); rope fp32 [max_pos, rot_dim] (rope_table); pools [num_pages, PS, Hkv, D]. Returns
     q_out [T, Hq, D] (q itself may be given, when contiguous)."""
     import torch
-    if not isinstance(q, torch.Tensor) or q.dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError("q must be a float16 or bfloat16 tensor")
+    device = _device_of(q, "q")
+    dt = q.dtype
+    if dt is not torch.float16 and dt is not torch.bfloat16:
+        raise TypeError("q must be float16 or bfloat16")
     if q.dim() != 3:
         raise ValueError("q must be [rows, Hq, D]")
-    dt = q.dtype
     T, Hq, D = q.shape
-    _require_cuda(k_pool, "k_pool", dt)
-    if k_pool.dim() != 4 or k_pool.shape[3] != D:
+    _require(k_pool, "k_pool", dt, None, device)
+    pool = k_pool.shape
+    if len(pool) != 4 or pool[3] != D:
         raise ValueError("k_pool must be [num_pages, page_size, Hkv, D]")
-    num_pages, PS, Hkv, _ = k_pool.shape
-    _require_cuda(v_pool, "v_pool", dt, k_pool.shape)
-    q_stride = _require_rows(q, "q", dt, (T, Hq, D))
-    k_stride = _require_rows(k, "k", dt, (T, Hkv, D))
-    v_stride = _require_rows(v, "v", dt, (T, Hkv, D))
-    _require_cuda(positions, "positions", torch.int32, (T,))
-    _require_cuda(slots, "slots", torch.int32, (T,))
-    _require_cuda(rope, "rope", torch.float32)
+    num_pages, PS, Hkv, _ = pool
+    _require(v_pool, "v_pool", dt, pool, device)
+    q_stride = _require_rows(q, "q", dt, (T, Hq, D), device)
+    k_stride = _require_rows(k, "k", dt, (T, Hkv, D), device)
+    v_stride = _require_rows(v, "v", dt, (T, Hkv, D), device)
+    _require(positions, "positions", torch.int32, (T,), device)
+    _require(slots, "slots", torch.int32, (T,), device)
+    _require(rope, "rope", torch.float32, None, device)
     if rope.dim() != 2:
         raise ValueError("rope must be [max_pos, rot_dim]")
-    weights = [w for w in (q_weight, k_weight) if w is not None]
-    for w in weights:
-        _require_cuda(w, "q_weight and k_weight", None, (D,))
-        if w.dtype != weights[0].dtype or w.dtype not in (dt, torch.float32):
-            raise TypeError(f"q_weight and k_weight must both be {dt} or both float32")
+    qw = kw = wt = None
+    for w in (q_weight, k_weight):
+        if w is not None:
+            wt = wt or (dt if isinstance(w, torch.Tensor) and w.dtype is dt else torch.float32)
+            _require(w, "q_weight and k_weight (both of q's type or both float32)", wt, (D,),
+                     device)
+    if q_weight is not None:
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        kw = k_weight.data_ptr()
     if q_out is None:
         q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
         _used_on(stream, q_out)
     else:
-        _require_cuda(q_out, "q_out", dt, (T, Hq, D))
-    device = _same_device(q, k, v, positions, slots, rope, k_pool, v_pool, q_out, *weights)
+        _require(q_out, "q_out", dt, (T, Hq, D), device)
     _call(device, stream, load_library().pa_qk_rope_append, "pa_qk_rope_append", Hq, Hkv, D, PS,
-          _dtype_code(dt), T, q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(),
-          v_stride, positions.data_ptr(), slots.data_ptr(), rope.data_ptr(), rope.shape[1],
-          rope.shape[0], 1 if interleaved else 0,
-          None if q_weight is None else q_weight.data_ptr(),
-          None if k_weight is None else k_weight.data_ptr(),
-          1 if weights and weights[0].dtype == torch.float32 else 0, eps, q_out.data_ptr(),
-          k_pool.data_ptr(), v_pool.data_ptr(), num_pages)
+          PA_BF16 if dt is torch.bfloat16 else PA_F16, T, q.data_ptr(), q_stride, k.data_ptr(),
+          k_stride, v.data_ptr(), v_stride, positions.data_ptr(), slots.data_ptr(),
+          rope.data_ptr(), rope.shape[1], rope.shape[0], 1 if interleaved else 0, qw, kw,
+          1 if wt is torch.float32 else 0, eps, q_out.data_ptr(), k_pool.data_ptr(),
+          v_pool.data_ptr(), num_pages)
     return q_out
 
 

@@ -442,11 +442,11 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& tm_k, const CUten
   }
 }
 
-template <int D, bool BF16, bool WIN>
+template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
     decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const PrefillArgs a) {
-  decode_body<D, BF16, false, WIN>(tm_k, tm_v, a, nullptr);
+  decode_body<D, BF16, false, false>(tm_k, tm_v, a, nullptr);
 }
 
 template <int D, bool BF16, bool WIN>

@@ -1,0 +1,747 @@
+// decode_stream.cuh — one query token per sequence over part of its keys (a window and sinks, or
+// the keys past a shared prefix), device lengths, groups of G <= 8 heads at head dim 128 or 256:
+// the products and the softmax of decode_kernel.cuh (keys on the MMA's M side) in a kernel that
+// stays for the whole step. Included by pa_kernels.cu.
+//
+// A unit is (sequence b, KV head g) with its list of n_b KV tiles (kv_tile). The units are laid
+// end to end, b-major, each n_b + 1 slots long (its start, worth about a tile: measured 2.6 us
+// at D 128 and 5 us at D 256 for the epilogue and the first loads, against 2.9 and 5 us a tile
+// with all CTAs streaming; then its tiles), T slots in all, and CTA c of C takes the c-th of C
+// equal runs of slots: a list of segments, each a unit or a part of one. Every CTA gets the same
+// work whatever the lengths are, and its copy warps go on into the next segment while the softmax
+// warps finish the last one. (One CTA per unit and split pays each unit's start and end in full
+// and fills its last wave in part: 32 sequences, window 4,096, D 256: 71 us at 10 splits, 54 us
+// at the best count, 4, against 40 us of K/V traffic.)
+//
+// Each CTA finds its run by itself: a block scan of the units' slots over runs of sequences (one
+// each up to 256), then a walk. A segment that is a whole unit writes its output rows; a part of
+// a unit leaves its rows and base-2 LSE in the CTA's workspace slot 0 (the CTA's first segment)
+// or 1 (its last), which merge_stream_kernel joins after the same scan.
+
+constexpr int kStreamRuns = 256;  // runs of sequences in the scan (= threads of both kernels)
+static_assert(kStreamRuns == kThreads, "one run a thread");
+
+template <int D>
+struct StreamCfg {
+  static constexpr int NP = D / 64;
+  static constexpr int NSLOT = kDecSlots;
+  static constexpr int Q_OFF = 0;                          // 2 buffers x NP atoms of 8 rows
+  static constexpr int P_OFF = Q_OFF + 2 * NP * 1024;      // 2 buffers x 2 panels x 1 KB
+  static constexpr int RING_OFF = P_OFF + 2 * 2 * 1024;
+  static constexpr int BAR_OFF = RING_OFF + NSLOT * kPanel;
+  static constexpr int B_FULL = 0, B_EMPTY = NSLOT, B_QFULL = 2 * NSLOT, B_SFULL = 2 * NSLOT + 2,
+                       B_PFULL = 2 * NSLOT + 4, B_PVDONE = 2 * NSLOT + 6,
+                       B_MMADONE = 2 * NSLOT + 8, N_BARS = 2 * NSLOT + 9;
+  static constexpr int RED_OFF = BAR_OFF + 8 * (N_BARS + 1);  // [2][4 warps][8 heads]
+  static constexpr int SUM_OFF = RED_OFF + 2 * 4 * 8 * 4;     // [4 warps][8 heads]
+  static constexpr int RUN_OFF = SUM_OFF + 4 * 8 * 4;         // [kStreamRuns + 1] int64
+  static constexpr int MISC_OFF = RUN_OFF + 8 * (kStreamRuns + 1);
+  static constexpr int SMEM = MISC_OFF + 16;
+  static constexpr int LAUNCH_SMEM = SMEM + 1024;
+  static constexpr int PANEL_LOG = (NP == 4) ? 9 : 8;
+  static_assert(BAR_OFF % 8 == 0 && RUN_OFF % 8 == 0, "alignment");
+  static_assert(kDecCtasPerSm * (LAUNCH_SMEM + 1024) <= 233472, "two CTAs per SM");
+};
+
+// Slots of a unit of n tiles (none without tiles), and sequences of a run of the scan.
+__device__ __forceinline__ int64_t stream_slots(int64_t n) { return n > 0 ? n + 1 : 0; }
+__device__ __forceinline__ int stream_per(const PrefillArgs& a) {
+  return (int)(((int64_t)a.batch + kStreamRuns - 1) / kStreamRuns);
+}
+// x / y for x >= 0, y > 0, in 32 bits where both fit (a 64-bit division is ~600 cycles).
+__device__ __forceinline__ int64_t div_pos(int64_t x, int64_t y) {
+  if (((x | y) >> 32) == 0) return (int64_t)((uint32_t)x / (uint32_t)y);
+  return x / y;
+}
+
+// Slots before every run of sequences (run i: sequences [i per, (i + 1) per)), in all heads, into
+// run[0 .. kStreamRuns]; `wsum`: a word per warp. Every thread of the block (kStreamRuns of
+// them). Reports bad lengths when `report`.
+__device__ __forceinline__ void stream_scan(const PrefillArgs& a_in, int64_t* run, int64_t* wsum,
+                                            bool report) {
+  PrefillArgs a = a_in;
+  const int t = threadIdx.x, lane = t & 31, wid = t >> 5;
+  const int per = stream_per(a);
+  const int64_t b0 = (int64_t)t * per, b1 = b0 + per < a.batch ? b0 + per : a.batch;
+  bool bad = false;
+  int64_t sum = 0;
+  for (int64_t b = b0; b < b1; ++b)
+    sum += stream_slots(stream_seq(a, b, &bad)) * a.Hkv;
+  if (bad && report) atomicOr(&g_pa_error_flags, kFlagPage);
+  int64_t incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) wsum[wid] = incl;
+  __syncthreads();
+  int64_t before = 0;
+  for (int w = 0; w < wid; ++w) before += wsum[w];
+  run[t + 1] = before + incl;
+  if (t == 0) run[0] = 0;
+  __syncthreads();
+}
+
+// The equal runs: C CTAs (two slots at least each: one tile a CTA adds more to the merge than it
+// saves; one sequence at window 4,096 measured 16.5 us at two, 18.6 us at one) of q slots, the
+// first r of them q + 1.
+struct StreamShare {
+  int64_t C, q, r;
+  __device__ __forceinline__ StreamShare(int64_t T, int64_t ctas) {
+    C = T / 2 < ctas ? T / 2 : ctas;
+    q = C > 0 ? div_pos(T, C) : 0;
+    r = T - q * C;
+  }
+  __device__ __forceinline__ int64_t first(int64_t c) const { return c * q + (c < r ? c : r); }
+  __device__ __forceinline__ int64_t owner(int64_t x) const {
+    const int64_t big = r * (q + 1);
+    return x < big ? div_pos(x, q + 1) : r + div_pos(x - big, q);
+  }
+};
+
+// A CTA's walk along its segments.
+struct StreamWalk {
+  int64_t b;        // sequence
+  int g;            // KV head
+  int64_t n_b;      // tiles of the unit
+  int64_t t0;       // first tile of the segment in the unit
+  int64_t left;     // slots of the CTA's run behind this segment
+  int n;            // tiles of the segment
+  int index;        // segments before this one
+};
+
+// The segment at slot x of the whole list (a: pointed at its sequence) of a run of `slots`.
+__device__ __forceinline__ StreamWalk stream_start(PrefillArgs& a, const int64_t* run, int64_t x,
+                                                   int64_t slots) {
+  StreamWalk s;
+  int lo = 0, hi = kStreamRuns - 1;
+  while (lo < hi) {  // the last run that begins at or before x
+    const int mid = (lo + hi + 1) >> 1;
+    if (run[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  bool bad;
+  s.b = (int64_t)lo * stream_per(a);
+  int64_t off = x - run[lo];
+  for (;; ++s.b) {
+    s.n_b = stream_seq(a, s.b, &bad);
+    const int64_t all = stream_slots(s.n_b) * a.Hkv;
+    if (off < all || s.b + 1 >= a.batch) break;
+    off -= all;
+  }
+  s.g = (int)div_pos(off, s.n_b + 1);
+  off -= s.g * (s.n_b + 1);
+  const int64_t mine = s.n_b + 1 - off < slots ? s.n_b + 1 - off : slots;
+  s.left = slots - mine;
+  s.t0 = off > 0 ? off - 1 : 0;
+  s.n = (int)(off > 0 ? mine : mine - 1);  // >= 1: a run has two slots at least
+  s.index = 0;
+  return s;
+}
+__device__ __forceinline__ bool stream_next(PrefillArgs& a, StreamWalk& s) {
+  if (s.left <= 1) return false;  // one slot: the start of a unit that the next CTA has
+  s.t0 = 0;
+  ++s.index;
+  if (++s.g == a.Hkv) {
+    s.g = 0;
+    bool bad;
+    do {
+      if (s.b + 1 >= a.batch) return false;
+      s.n_b = stream_seq(a, ++s.b, &bad);
+    } while (s.n_b == 0);
+  }
+  const int64_t mine = s.n_b + 1 < s.left ? s.n_b + 1 : s.left;
+  s.left -= mine;
+  s.n = (int)(mine - 1);
+  return true;
+}
+// Point a's table row and its length at the walk's sequence.
+__device__ __forceinline__ void stream_table(PrefillArgs& a, const PrefillArgs& a0, int64_t b) {
+  a.page_table = a0.page_table + b * a.table_stride;
+  a.table_len = (a.total_keys + a.page_rows - 1) / a.page_rows;
+}
+
+// Copy warp w of kIssuers: the K/V tiles of all segments through the ring, as kv_copy_role does
+// for one unit (K0, K1, V0, K2, V1, ..., V_{n-1} within a segment, fill numbers running on).
+template <int NP, int NSLOT, int PANEL_LOG>
+__device__ __forceinline__ void stream_copy_role(const PrefillArgs& a0, const CUtensorMap* tm_k,
+                                                 const CUtensorMap* tm_v, const int64_t* run,
+                                                 int64_t x0, int64_t slots, int w, uint32_t ring,
+                                                 uint32_t bar_full, uint32_t bar_empty,
+                                                 volatile int* abort_flag, uint64_t tmo) {
+  PrefillArgs a = a0, an = a0;  // at the segment's sequence, and at the next one's
+  const int lane = threadIdx.x & 31;
+  auto slot_addr = [&](uint32_t slot) -> uint32_t { return ring + slot * kPanel; };
+  auto full = [&](uint32_t slot) -> uint32_t { return bar_full + 8u * slot; };
+  const int ppt = a.pages_per_tile, prow = a.page_rows;
+  const int vsub = prow >> a.v_shift;             // V boxes per page
+  const int vbytes_log = a.v_shift + PANEL_LOG;   // log2 of a V box's bytes
+  const int vbox_per_slot = 1 << (14 - vbytes_log);
+  bool ok = true;
+  auto acquire = [&](uint32_t q) -> bool {
+    const uint32_t slot = q % NSLOT;
+    const bool r_ok = q < (uint32_t)NSLOT ||
+                      warp_wait(bar_empty + 8u * slot, ((q / NSLOT) - 1) & 1, abort_flag, tmo);
+    if (r_ok && lane == 0) mbar_arrive_expect_tx(full(slot), kPanel);
+    __syncwarp();
+    return r_ok;
+  };
+  uint32_t base = 0, issued_end = 0;  // fills of the segments before; one past the last issued
+  auto fetch = [&](const PrefillArgs& at, const StreamWalk& seg, int jt) -> int32_t {
+    return tile_page_row<true, true>(at, seg.t0, seg.n, jt, lane, w == 0);
+  };
+  StreamWalk s = stream_start(a, run, x0, slots);
+  stream_table(a, a0, s.b);
+  int32_t row_cur = fetch(a, s, 0), row_next = fetch(a, s, 1);
+  for (bool more = true; more && ok;) {
+    const int n = s.n;
+    // the next segment's first table entries are read a segment ahead
+    StreamWalk nx = s;
+    an = a;
+    more = stream_next(an, nx);
+    int32_t next_0 = a.oob_row, next_1 = a.oob_row;
+    if (more) {
+      stream_table(an, a0, nx.b);
+      next_0 = fetch(an, nx, 0);
+      next_1 = fetch(an, nx, 1);
+    }
+    int32_t row_prev = a.oob_row;
+    for (int j = 0; j <= n && ok; ++j) {
+      if (j < n) {
+        const uint32_t item = j == 0 ? 0u : 2u * j - 1u;
+        for (int k = 0; k < NP && ok; ++k) {
+          const uint32_t q = base + item * NP + k;
+          if ((int)(q % kIssuers) != w) continue;
+          if (!(ok = acquire(q))) break;
+          const uint32_t slot = q % NSLOT;
+          if (lane < ppt)
+            tma_load_3d(slot_addr(slot) + lane * prow * 128, tm_k, full(slot), k * 64, s.g,
+                        row_cur);
+          issued_end = q + 1;
+        }
+      }
+      if (ok && j >= 1) {
+        const uint32_t item = v_item(j - 1, n);
+        for (int k = 0; k < NP && ok; ++k) {
+          const uint32_t q = base + item * NP + k;
+          if ((int)(q % kIssuers) != w) continue;
+          if (!(ok = acquire(q))) break;
+          const uint32_t slot = q % NSLOT;
+          const int bx = k * vbox_per_slot + lane;
+          const int pg = bx / vsub, sub = bx - pg * vsub;
+          const int32_t prow_b = __shfl_sync(0xffffffffu, row_prev, pg & 31);
+          if (lane < vbox_per_slot)
+            tma_load_4d(slot_addr(slot) + (lane << vbytes_log), tm_v, full(slot), 0,
+                        prow_b + (sub << a.v_shift), 0, s.g);
+          issued_end = q + 1;
+        }
+      }
+      row_prev = row_cur;
+      row_cur = row_next;
+      row_next = fetch(a, s, j + 2);
+    }
+    base += 2u * (uint32_t)n * NP;
+    s = nx;
+    a = an;
+    row_cur = next_0;
+    row_next = next_1;
+  }
+  // every copy must land before the CTA may exit (see kv_copy_role)
+  for (uint32_t q = base > (uint32_t)NSLOT ? base - NSLOT : 0; q < issued_end; ++q)
+    if ((int)(q % kIssuers) == w)
+      drain_wait(full(q % NSLOT), (q / NSLOT) & 1, abort_flag, tmo);
+  __syncwarp();
+}
+
+// WHOLE: the result of a whole unit is the output (16-bit); else a partial too (its row and LSE at
+// row b Hq + head of the workspace's first batch * Hq rows, before the part slots).
+template <int D, bool BF16, bool WHOLE>
+__global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
+    decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a0) {
+  using C = StreamCfg<D>;
+  constexpr int NP = C::NP, NSLOT = C::NSLOT, NH = D / 128;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t* run = reinterpret_cast<int64_t*>(smem + C::RUN_OFF);
+  auto bar = [&](int i) -> uint32_t { return sb + C::BAR_OFF + 8u * (uint32_t)i; };
+  auto slot_addr = [&](uint32_t r) -> uint32_t { return sb + C::RING_OFF + r * kPanel; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF + 4);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NSLOT; ++i) {
+      mbar_init(bar(C::B_FULL + i), 1);
+      mbar_init(bar(C::B_EMPTY + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(C::B_QFULL + i), 4);
+      mbar_init(bar(C::B_SFULL + i), 1);
+      mbar_init(bar(C::B_PFULL + i), 4);
+      mbar_init(bar(C::B_PVDONE + i), 1);
+    }
+    mbar_init(bar(C::B_MMADONE), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == kMmaWarp + 1 && lane == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), kDecTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  // its barriers also publish the set-up above; `red` is not in use yet
+  stream_scan(a0, run, reinterpret_cast<int64_t*>(smem + C::RED_OFF), blockIdx.x == 0);
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const StreamShare share(run[kStreamRuns], gridDim.x);
+  if (blockIdx.x >= share.C) {
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kDecTmemCols);
+    return;
+  }
+  const int64_t x0 = share.first(blockIdx.x);
+  const int64_t slots = share.first(blockIdx.x + 1) - x0;
+  const uint64_t tmo = a0.timeout_ns;
+  PrefillArgs a = a0;
+
+  if (warp < 4) {
+    // ============================================================ softmax + epilogue
+    const int t = threadIdx.x;  // key t of each tile (S^T lane); dim t of each half (O^T lane)
+    const int G = a.G;          // <= 8
+    const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
+    // Q rows 0..7 of a segment (zeros past G) in its buffer, 128-byte swizzle, one atom per
+    // panel: 8 x D/8 pieces of 16 bytes, NP / 2 a thread. The next segment's are loaded at the
+    // start of a segment and stored after its first tile: by then the segment before, the
+    // buffer's last reader, has all its S.
+    uint4 qv[NP / 2];
+    auto q_load = [&](int64_t b, int g) {
+#pragma unroll
+      for (int i = 0; i < NP / 2; ++i) {
+        const int p = t + 128 * i, row = p / (D / 8), col = p % (D / 8);
+        qv[i] = row < G ? __ldg(reinterpret_cast<const uint4*>(
+                              a0.q + (b * a.Hq + g * G + row) * (int64_t)D) + col)
+                        : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    auto q_store = [&](int buf) {
+#pragma unroll
+      for (int i = 0; i < NP / 2; ++i) {
+        const int p = t + 128 * i, row = p / (D / 8), col = p % (D / 8);
+        st_shared_v4(sb + C::Q_OFF + buf * (NP * 1024) + (col >> 3) * 1024 + row * 128 +
+                         (((col & 7) ^ row) << 4),
+                     qv[i].x, qv[i].y, qv[i].z, qv[i].w);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::B_QFULL + buf));
+    };
+    float* red = reinterpret_cast<float*>(smem + C::RED_OFF);
+    float* sums = reinterpret_cast<float*>(smem + C::SUM_OFF);
+    bool ok = true;
+    uint32_t jj = 0;       // tiles of the segments before
+    uint32_t fills = 0;    // ring fills of the segments before
+    StreamWalk s = stream_start(a, run, x0, slots);
+    q_load(s.b, s.g);
+    q_store(0);
+    for (bool more = true; more && ok;) {
+      const int n = s.n;
+      const PrefillArgs as = a;  // this segment's sequence; `a` goes on to the next one
+      StreamWalk nx = s;
+      more = stream_next(a, nx);
+      if (more) q_load(nx.b, nx.g);
+      float m_run[8], l_part[8];
+#pragma unroll
+      for (int h = 0; h < 8; ++h) {
+        m_run[h] = -INFINITY;
+        l_part[h] = 0.f;
+      }
+      // PV of tile i (counted over all segments) completes phase i/2 of pv_done[i % 2]; the waits
+      // below observe every one, the two last of a segment at its end.
+      auto wait_pv = [&](uint32_t i) -> bool {
+        return warp_wait(bar(C::B_PVDONE + (i & 1)), (i >> 1) & 1, abort_flag, tmo);
+      };
+      for (int j = 0; j < n; ++j) {
+        const uint32_t i = jj + j;
+        const int sbuf = i & 1;
+        const int64_t key0 = kv_tile<true>(as, s.t0 + j) * kTileKeys;
+        const bool live = !key_unseen<true>(as, key0 + t);
+        float sv[8];
+        if (ok) ok = warp_wait(bar(C::B_SFULL + sbuf), (i >> 1) & 1, abort_flag, tmo);
+        if (ok) {
+          tc_fence_after();
+          tmem_ld8(t_lane + kDecSCol + 16u * sbuf, sv);
+          tmem_wait_ld();
+        }
+        float mx[8];
+#pragma unroll
+        for (int h = 0; h < 8; ++h) mx[h] = warp_max(ok && live ? sv[h] : -INFINITY);
+        if (lane == 0) {
+          float* r = red + sbuf * 32 + warp * 8;
+          *reinterpret_cast<float4*>(r) = make_float4(mx[0], mx[1], mx[2], mx[3]);
+          *reinterpret_cast<float4*>(r + 4) = make_float4(mx[4], mx[5], mx[6], mx[7]);
+        }
+        if (named_bar_or(kDecBarSoftmax, 128, !ok)) {
+          ok = false;
+          break;
+        }
+        float m_new[8];
+        bool need[8], any = false;
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+          const float* r = red + sbuf * 32 + h;
+          const float tm = fmaxf(fmaxf(r[0], r[8]), fmaxf(r[16], r[24]));
+          m_new[h] = fmaxf(m_run[h], tm * a.scale_log2);
+          need[h] = m_new[h] > m_run[h] + kRescaleLog2;
+          any |= need[h];
+        }
+        if (j == 0) {
+#pragma unroll
+          for (int h = 0; h < 8; ++h)
+            if (need[h]) m_run[h] = m_new[h];
+        } else if (any) {
+          ok = wait_pv(i - 1);  // O^T must not change under a running MMA
+          if (ok) {
+            tc_fence_after();
+            float f[8];
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+              f[h] = need[h] ? ex2(m_run[h] - m_new[h]) : 1.0f;
+              l_part[h] *= f[h];
+              if (need[h]) m_run[h] = m_new[h];
+            }
+#pragma unroll
+            for (int hf = 0; hf < NH; ++hf) {
+              float o[8];
+              tmem_ld8(t_lane + kDecOCol + 16u * hf, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int h = 0; h < 8; ++h) o[h] *= f[h];
+              tmem_st8(t_lane + kDecOCol + 16u * hf, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        float p[8];
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+          const float mu = m_run[h] == -INFINITY ? 0.f : m_run[h];
+          p[h] = ok && live ? ex2(fmaf(sv[h], a.scale_log2, -mu)) : 0.f;
+          l_part[h] += p[h];
+        }
+        if (ok && i >= 2) ok = wait_pv(i - 2);  // the last reader of P's buffer
+        if (ok && tile_unseen<true>(as, key0)) {
+          // V rows of keys that the row does not see may hold any bits; P is 0 there, but
+          // 0 * NaN is NaN inside the MMA, so those rows are zeroed. Once S(j+1) and PV(i-1)
+          // are done, every earlier fill of V(j)'s slots has landed (K up to K(j+1), V up to
+          // V(i-1); a segment's last tile follows K(j) directly), so the parity waits see
+          // V(j)'s own fills. Neither wait needs this P.
+          if (j + 1 < n)
+            ok = warp_wait(bar(C::B_SFULL + ((i + 1) & 1)), ((i + 1) >> 1) & 1, abort_flag, tmo);
+          if (ok && i >= 1) ok = wait_pv(i - 1);
+          const uint32_t seq0 = fills + v_item(j, n) * NP;
+          for (int q = 0; q < NP && ok; ++q)
+            ok = warp_wait(bar(C::B_FULL + (seq0 + q) % NSLOT), ((seq0 + q) / NSLOT) & 1,
+                           abort_flag, tmo);
+          if (ok && !live) {
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+              const uint32_t off = v_offset<NP, C::PANEL_LOG>((uint32_t)t, q, a.v_shift);
+              const uint32_t ra = slot_addr((seq0 + (off >> 14)) % NSLOT) + (off & (kPanel - 1));
+#pragma unroll
+              for (int c = 0; c < 8; ++c) st_shared_v4(ra + c * 16, 0u, 0u, 0u, 0u);
+            }
+          }
+        }
+        if (ok) {
+          const uint32_t pb = sb + C::P_OFF + (uint32_t)sbuf * 2048u + (uint32_t)(t >> 6) * 1024u;
+          const uint32_t chunk = (uint32_t)((t & 63) >> 3), sub = (uint32_t)(t & 7) * 2u;
+#pragma unroll
+          for (int h = 0; h < 8; ++h)
+            st_shared_u16(pb + h * 128u + ((chunk ^ (uint32_t)h) << 4) + sub, to16<BF16>(p[h]));
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(bar(C::B_PFULL + sbuf));
+        if (j == 0 && more) q_store((s.index + 1) & 1);
+      }
+
+      const uint32_t last = jj + n - 1;
+      if (ok && last >= 1) ok = wait_pv(last - 1);
+      if (ok) ok = wait_pv(last);
+      float ls[8];
+#pragma unroll
+      for (int h = 0; h < 8; ++h) ls[h] = warp_sum(l_part[h]);
+      if (lane == 0) {
+        *reinterpret_cast<float4*>(sums + warp * 8) = make_float4(ls[0], ls[1], ls[2], ls[3]);
+        *reinterpret_cast<float4*>(sums + warp * 8 + 4) = make_float4(ls[4], ls[5], ls[6], ls[7]);
+      }
+      if (named_bar_or(kDecBarSoftmax, 128, !ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float inv_l[8];
+#pragma unroll
+      for (int h = 0; h < 8; ++h) {
+        ls[h] = (sums[h] + sums[8 + h]) + (sums[16 + h] + sums[24 + h]);
+        inv_l[h] = ls[h] > 0.f ? __frcp_rn(ls[h]) : 0.f;
+      }
+      const bool whole = n == s.n_b;
+      const int64_t out_row = s.b * a.Hq + s.g * G;  // heads g G .. g G + G - 1
+      const int64_t row0 =
+          whole ? out_row
+                : (WHOLE ? 0 : (int64_t)a.batch * a.Hq) +
+                      (2 * (int64_t)blockIdx.x + (s.index > 0 ? 1 : 0)) * G;
+#pragma unroll
+      for (int hf = 0; hf < NH; ++hf) {
+        float o[8];
+        tmem_ld8(t_lane + kDecOCol + 16u * hf, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+          if (h >= G) continue;
+          const int64_t at = (row0 + h) * D + 128 * hf + t;
+          if (WHOLE && whole)
+            reinterpret_cast<uint16_t*>(a.out)[at] = to16<BF16>(o[h] * inv_l[h]);
+          else
+            a.ws_o[at] = o[h] * inv_l[h];
+        }
+      }
+      if (!(WHOLE && whole) && t < G) {
+        float m = m_run[0], l = ls[0];
+#pragma unroll
+        for (int h = 1; h < 8; ++h)
+          if (t == h) {
+            m = m_run[h];
+            l = ls[h];
+          }
+        a.ws_lse[row0 + t] = l > 0.f ? m + log2f(l) : -INFINITY;
+      }
+      // O^T is read: the next segment's first PV waits for a P that comes after this.
+      tc_fence_before();
+      jj += n;
+      fills += 2u * (uint32_t)n * NP;
+      s = nx;
+    }
+  } else if (warp > kMmaWarp) {
+    // ============================================================ TMA issuers (three warps)
+    stream_copy_role<NP, NSLOT, C::PANEL_LOG>(a0, &tm_k, &tm_v, run, x0, slots,
+                                              warp - kMmaWarp - 1, sb + C::RING_OFF,
+                                              bar(C::B_FULL), bar(C::B_EMPTY), abort_flag, tmo);
+  } else {
+    // ============================================================ MMA issuer (one lane)
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = umma_idesc_f16(128, kDecN, BF16, false, false);
+      constexpr uint32_t idesc_pv = umma_idesc_f16(128, kDecN, BF16, false, true);
+      constexpr uint32_t kSlotDesc = kPanel >> 4;
+      const uint64_t q_desc0 = smem_desc_sw128(sb + C::Q_OFF, 16, 0);
+      const uint64_t p_desc = smem_desc_sw128(sb + C::P_OFF, 16, 0);
+      const uint64_t k_desc = smem_desc_sw128(sb + C::RING_OFF, 16, 1024);
+      const uint64_t v_desc = smem_desc_sw128(sb + C::RING_OFF, (uint32_t)a.v_rows * 128u, 1024);
+      uint32_t slot = 0, round = 0, jj = 0;
+      bool ok = true;
+      StreamWalk s = stream_start(a, run, x0, slots);
+      do {
+        const int n = s.n;
+        const uint64_t q_desc = q_desc0 + (uint32_t)(s.index & 1) * (NP * 1024 >> 4);
+        ok = thread_wait(bar(C::B_QFULL + (s.index & 1)), (s.index >> 1) & 1, abort_flag, tmo);
+        tc_fence_after();
+        for (int j = 0; j <= n && ok; ++j) {
+          if (j < n) {
+            // S^T of tile i is written over that of tile i - 2, which the softmax read before it
+            // released P(i-2) (the PV MMA that read P(i-2) was issued before this one).
+            const uint32_t i = jj + j;
+            const uint32_t s_tmem = tmem + kDecSCol + 16u * (i & 1);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+              ok = thread_wait(bar(C::B_FULL + slot), round & 1, abort_flag, tmo);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t ad = k_desc + slot * kSlotDesc, bd = q_desc + p * (1024 >> 4);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_ss(s_tmem, ad + 2 * kk, bd + 2 * kk, idesc_qk, (p | kk) != 0 ? 1u : 0u);
+              umma_commit(bar(C::B_EMPTY + slot));
+              if (++slot == (uint32_t)NSLOT) {
+                slot = 0;
+                ++round;
+              }
+            }
+            if (!ok) break;
+            umma_commit(bar(C::B_SFULL + (i & 1)));
+          }
+          if (j >= 1) {
+            const uint32_t i = jj + j - 1;
+            ok = thread_wait(bar(C::B_PFULL + (i & 1)), (i >> 1) & 1, abort_flag, tmo);
+            const uint32_t vslot0 = slot;
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+              if (ok) ok = thread_wait(bar(C::B_FULL + slot), round & 1, abort_flag, tmo);
+              if (++slot == (uint32_t)NSLOT) {
+                slot = 0;
+                ++round;
+              }
+            }
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < kTileKeys / 16; ++ks) {
+              const uint64_t bd = p_desc + (i & 1) * (2048 >> 4) + (ks >> 2) * (1024 >> 4) +
+                                  (ks & 3) * 2;
+#pragma unroll
+              for (int hf = 0; hf < NH; ++hf) {
+                const uint32_t off = v_offset<NP, C::PANEL_LOG>(16u * ks, 2u * hf, a.v_shift);
+                uint32_t vs = vslot0 + (off >> 14);
+                if (vs >= (uint32_t)NSLOT) vs -= NSLOT;
+                umma_ss(tmem + kDecOCol + 16u * hf,
+                        v_desc + vs * kSlotDesc + ((off & (kPanel - 1)) >> 4), bd, idesc_pv,
+                        (j > 1 || ks > 0) ? 1u : 0u);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+              uint32_t vs = vslot0 + k;
+              if (vs >= (uint32_t)NSLOT) vs -= NSLOT;
+              umma_commit(bar(C::B_EMPTY + vs));
+            }
+            umma_commit(bar(C::B_PVDONE + (i & 1)));
+          }
+        }
+        jj += n;
+      } while (ok && stream_next(a, s));
+      // Every issued MMA must finish before tensor memory is freed.
+      umma_commit(bar(C::B_MMADONE));
+      drain_wait(bar(C::B_MMADONE), 0, abort_flag, tmo);
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kDecTmemCols);
+  }
+}
+
+// The units that the stream kernel cut, and the sequences without a key (zeros): one warp an
+// output row (b, head). The row's parts sit in the slots of CTAs c0 .. c1, those whose runs hold
+// tiles of the unit: slot 0 of each, or slot 1 of c0 when the unit is not the first of its run.
+// PREFIX: n_pre partials of the shared prefix ([n_pre][batch * Hq] rows before the rest of the
+// workspace) join, and a whole unit's partial is read from its own row.
+template <int D, int OUT, bool PREFIX>
+__global__ void __launch_bounds__(kStreamRuns) merge_stream_kernel(const PrefillArgs a0,
+                                                                   int64_t grid_ctas,
+                                                                   const float* pre_o,
+                                                                   const float* pre_lse,
+                                                                   int n_pre) {
+  __shared__ int64_t run[kStreamRuns + 1], wsum[kStreamRuns / 32];
+  stream_scan(a0, run, wsum, false);
+  // Launched while the stream kernel ends (programmatic launch): its results are complete past
+  // this wait. The lengths above were there before it.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const StreamShare share(run[kStreamRuns], grid_ctas);
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = (int64_t)a0.batch * a0.Hq;
+  const int per = stream_per(a0);
+  PrefillArgs a = a0;
+  constexpr int NV = D / 128;  // float4 columns a lane holds
+  for (int64_t row = (int64_t)blockIdx.x * (kStreamRuns / 32) + threadIdx.x / 32; row < rows;
+       row += (int64_t)gridDim.x * (kStreamRuns / 32)) {
+    const int64_t b = div_pos(row, a.Hq), in_run = div_pos(b, per);
+    const int head = (int)(row - b * a.Hq), g = head / a.G;
+    bool bad;
+    int64_t off = run[in_run];  // the unit's first slot (its start; its tiles follow)
+    for (int64_t c = in_run * per; c < b; ++c)
+      off += stream_slots(stream_seq(a, c, &bad)) * a.Hkv;
+    const int64_t n_b = stream_seq(a, b, &bad);
+    off += g * (n_b + 1);
+    int64_t c0 = 0, np = 0;  // parts of the unit
+    bool whole = false, late = false;
+    if (n_b > 0) {
+      c0 = share.owner(off + 1);
+      np = share.owner(off + n_b) - c0 + 1;
+      whole = np == 1;
+      late = share.first(c0) < off;  // the run begins in an earlier unit
+    }
+    if (!PREFIX && whole) continue;  // the stream kernel wrote the output
+    // Part p: of the prefix (p < n_pre), else of the unit.
+    const int64_t unit0 = PREFIX ? rows : 0;  // rows of the workspace before the part slots
+    const int64_t total = (PREFIX ? n_pre : 0) + np;
+    auto place = [&](int64_t p, const float** o, const float** lse) {
+      if (PREFIX && p < n_pre) {
+        *o = pre_o + (p * rows + row) * D;
+        *lse = pre_lse + p * rows + row;
+        return;
+      }
+      const int64_t i = p - (PREFIX ? n_pre : 0);
+      const int64_t r = whole ? row
+                              : unit0 + (2 * (c0 + i) + (i == 0 && late ? 1 : 0)) * a.G +
+                                    (head - g * a.G);
+      *o = a.ws_o + r * D;
+      *lse = a.ws_lse + r;
+    };
+    auto lse_of = [&](int64_t p) -> float {
+      const float *o, *lse;
+      if (p >= total) return -INFINITY;
+      place(p, &o, &lse);
+      return *lse;
+    };
+    const float lse0 = lse_of(lane);  // part `lane`; more than 32 are read again below
+    float M = lse0;
+    for (int64_t p = 32 + lane; p < total; p += 32) M = fmaxf(M, lse_of(p));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float W = 0.f;
+    float4 acc[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kGroup = 8 / NV;  // parts loaded together
+    for (int64_t p32 = 0; M != -INFINITY && p32 < total; p32 += 32) {
+      const float lse = p32 == 0 ? lse0 : lse_of(p32 + lane);
+      const float wl = lse == -INFINITY ? 0.f : exp2f(lse - M);
+      const int np32 = total - p32 < 32 ? (int)(total - p32) : 32;
+      for (int p0 = 0; p0 < np32; p0 += kGroup) {
+        float4 x[kGroup][NV];
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k) {
+          if (p0 + k >= np32) continue;
+          const float *o, *l;
+          place(p32 + p0 + k, &o, &l);
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+            x[k][v] = *reinterpret_cast<const float4*>(o + lane * 4 + 128 * v);
+        }
+#pragma unroll
+        for (int k = 0; k < kGroup; ++k) {
+          const float w = __shfl_sync(0xffffffffu, wl, (p0 + k) & 31);
+          if (p0 + k >= np32 || w == 0.f) continue;
+          W += w;
+#pragma unroll
+          for (int v = 0; v < NV; ++v) {
+            acc[v].x = fmaf(w, x[k][v].x, acc[v].x);
+            acc[v].y = fmaf(w, x[k][v].y, acc[v].y);
+            acc[v].z = fmaf(w, x[k][v].z, acc[v].z);
+            acc[v].w = fmaf(w, x[k][v].w, acc[v].w);
+          }
+        }
+      }
+    }
+    const float inv = W > 0.f ? 1.f / W : 0.f;
+    uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + row * D;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      *reinterpret_cast<uint2*>(dst + lane * 4 + 128 * v) =
+          make_uint2(pack2<OUT == kOutBf16>(acc[v].x * inv, acc[v].y * inv),
+                     pack2<OUT == kOutBf16>(acc[v].z * inv, acc[v].w * inv));
+  }
+}

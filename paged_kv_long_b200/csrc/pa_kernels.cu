@@ -104,6 +104,7 @@ struct PrefillArgs {
   // v + tile_gap).
   int64_t window, sinks;
   int64_t win_lo, tile_head, tile_gap;
+  int64_t first_key;       // WIN: keys below it are not this launch's (a shared prefix's)
 };
 
 // KV tile of entry t of the unit's tile list.
@@ -372,7 +373,8 @@ struct SoftmaxCtx {
 // together with its base-2 log-sum-exp. The row goes through shared memory (x.stage_off, idle
 // once the last P V is done; rows 16 bytes apart from a multiple of 128 so that a warp's
 // stores spread over the banks) and leaves as one contiguous bulk copy.
-template <int D, bool WIN, bool BF16>
+// PRE (shared prefix): always a partial.
+template <int D, bool WIN, bool PRE, bool BF16>
 __device__ __forceinline__ void write_row(const PrefillArgs& a, const SoftmaxCtx& x, int r,
                                           bool valid, int64_t tok, int head, float m_run,
                                           float l_run, uint32_t t_lane) {
@@ -380,7 +382,7 @@ __device__ __forceinline__ void write_row(const PrefillArgs& a, const SoftmaxCtx
   int64_t ws_row = -1;  // workspace row of a partial; -1: the final output
   if (x.slot >= 0)
     ws_row = (int64_t)x.slot * a.rows_per_block + x.row0 + r;
-  else if (x.slot == kSlotUniform && a.splits > 1)
+  else if (x.slot == kSlotUniform && (PRE || a.splits > 1))
     ws_row = (int64_t)x.s * a.ws_split_rows + tok * a.Hq + head;
   float* dst = ws_row < 0 ? out_at<WIN>(a.out, (tok * a.Hq + head) * (int64_t)D)
                           : a.ws_o + ws_row * D;
@@ -414,11 +416,13 @@ __device__ __forceinline__ void write_row(const PrefillArgs& a, const SoftmaxCtx
   if (valid && ws_row >= 0) a.ws_lse[ws_row] = l_run > 0.f ? m_run + log2f(l_run) : -INFINITY;
 }
 
-// The window's lower limit on a row's scores of the tile at key0, by select: keys below the
-// row's window (limit - window + 1 - key0 keys in, limit its last key) that are no sinks.
+// The lower limit on a row's scores of the tile at key0, by select: keys below the row's window
+// (limit its last key) or this launch's first key that are no sinks.
 __device__ __forceinline__ void mask_window(const PrefillArgs& a, int64_t limit, int64_t key0,
                                             float (&sv)[kTileKeys]) {
-  const int64_t below = limit + 1 - a.window - key0;
+  int64_t below = limit + 1 - a.window;
+  if (below < a.first_key) below = a.first_key;
+  below -= key0;
   if (below <= 0) return;
   const int end = below < kTileKeys ? (int)below : kTileKeys;
   const int64_t snk = a.sinks - key0;
@@ -428,7 +432,18 @@ __device__ __forceinline__ void mask_window(const PrefillArgs& a, int64_t limit,
     if (c >= first && c < end) sv[c] = -INFINITY;
 }
 
-template <int D, bool PAGED, bool BF16, bool SQ, bool WIN, class VTail>
+// The last key that the row of token tok sees. PRE: token tok is sequence tok's one query row,
+// which sees the shared prefix (total_keys) as far as its sequence goes.
+template <bool PRE>
+__device__ __forceinline__ int64_t row_limit(const PrefillArgs& a, int64_t tok) {
+  if constexpr (PRE) {
+    const int64_t len = __ldg(a.seq_lens + tok);
+    return (len < a.total_keys ? len : a.total_keys) - 1;
+  }
+  return a.hist_len + tok;
+}
+
+template <int D, bool PAGED, bool BF16, bool SQ, bool WIN, bool PRE, class VTail>
 __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const SoftmaxCtx& x,
                                              VTail&& v_tail) {
   constexpr int NP = D / 64;
@@ -473,7 +488,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Softmax
       if (lane == 0) arrive(x.arrive_qfull);
     }
 
-    const int64_t limit = valid ? a.hist_len + tok : -1;  // last key this row may see
+    const int64_t limit = valid ? row_limit<PRE>(a, tok) : -1;  // last key this row may see
     const uint32_t t_lane = tmem + ((uint32_t)(warp * 32) << 16);
     const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
     float m_run = -INFINITY;  // running max of scale*log2(e)*score
@@ -602,7 +617,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Softmax
     if (ok) ok = warp_wait(x.bar_pvdone + 8u * ((n - 1) & 1), ((n - 1) >> 1) & 1, abort_flag, tmo);
     if (ok) {
       tc_fence_after();
-      write_row<D, WIN, BF16>(a, x, r, valid, tok, head, m_run, l_run, t_lane);
+      write_row<D, WIN, PRE, BF16>(a, x, r, valid, tok, head, m_run, l_run, t_lane);
     }
   }
 }
@@ -640,6 +655,28 @@ __device__ __forceinline__ int32_t tile_page_row(const PrefillArgs& a, int64_t k
   return row;
 }
 
+// The keys of sequence b (clamped into the table row; *bad: they were outside) and its tile list,
+// set in a: total_keys, win_lo, tile_head, tile_gap. Returns the number of tiles.
+__device__ __forceinline__ int64_t stream_seq(PrefillArgs& a, int64_t b, bool* bad) {
+  int64_t len = __ldg(a.seq_lens + b);
+  const int64_t cap = (int64_t)a.table_stride * a.page_rows;
+  if (len < 0 || len > cap) {
+    *bad = true;
+    len = len < 0 ? 0 : cap;
+  }
+  a.total_keys = len;
+  if (len <= a.first_key) return 0;
+  int64_t n;
+  a.win_lo = window_lo(len - 1, a.window);
+  if (a.first_key > a.win_lo) a.win_lo = a.first_key;
+  const int64_t w0 = a.win_lo / kTileKeys;
+  const int64_t hs = ceil_div64(a.sinks < len ? a.sinks : len, kTileKeys);
+  a.tile_head = hs;
+  a.tile_gap = hs < w0 ? w0 - hs : 0;
+  n = (len - 1) / kTileKeys + 1 - a.tile_gap;
+  return n;
+}
+
 // Device-length decode, block blockIdx.x: unit (sequence of rank blockIdx.x / (Hkv·S), KV head
 // g, split s) over its keys 0 .. len-1 (the new token's own included, all visible). Points a at
 // the sequence (Q, output and workspace rows, page-table row, lengths) and gives the unit's KV
@@ -665,6 +702,7 @@ __device__ __forceinline__ void decode_unit(PrefillArgs& a, int32_t* scratch, in
     if (threadIdx.x == 0 && *g == 0 && *s == 0) atomicOr(&g_pa_error_flags, kFlagPage);
     len = len < 0 ? 0 : cap;
   }
+  const int64_t seq = b;
   a.q += b * a.Hq * D;
   a.out = out_at<WIN>(a.out, b * a.Hq * D);
   if (a.ws_o) {
@@ -677,12 +715,8 @@ __device__ __forceinline__ void decode_unit(PrefillArgs& a, int32_t* scratch, in
   a.table_len = (len + a.page_rows - 1) / a.page_rows;
   a.R = len > 0 ? 1 : 0;
   if constexpr (WIN) {
-    int64_t n = 0;
-    if (len > 0) {
-      a.win_lo = window_lo(len - 1, a.window);
-      window_tiles(len - 1, len - 1, a.window, a.sinks, &a.tile_head, &a.tile_gap, &n);
-    }
-    split_range(n, *s, a.splits, kt0, kt1);
+    bool bad;
+    split_range(stream_seq(a, seq, &bad), *s, a.splits, kt0, kt1);
     return;
   }
   split_range((len + kTileKeys - 1) / kTileKeys, *s, a.splits, kt0, kt1);
@@ -802,7 +836,7 @@ __device__ __forceinline__ void kv_copy_role(const PrefillArgs& a, const CUtenso
 }
 
 // ---------------------------------------------------------------- prefill kernel
-template <int D, bool PAGED, bool BF16, bool SQ, bool WIN>
+template <int D, bool PAGED, bool BF16, bool SQ, bool WIN, bool PRE>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                    const PrefillArgs a_in, const __grid_constant__ ItemTable items) {
@@ -833,7 +867,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     qt = 0;
   } else {
     unit_coords(blockIdx.x, a.q_tiles, a.Hkv, a.splits, &qt, &g, &s);
-    split_range(tile_kv_tiles(qt, a.R, a.G, a.hist_len), s, a.splits, &kt0, &kt1);
+    split_range(PRE ? ceil_div64(a.total_keys, kTileKeys)
+                    : tile_kv_tiles(qt, a.R, a.G, a.hist_len),
+                s, a.splits, &kt0, &kt1);
   }
   const int n = (int)(kt1 - kt0);
 
@@ -926,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       return true;
     };
-    softmax_role<D, PAGED, BF16, SQ, WIN>(a, sc, v_tail);
+    softmax_role<D, PAGED, BF16, SQ, WIN, PRE>(a, sc, v_tail);
   } else if (warp > kMmaWarp) {
     // ============================================================ TMA issuers (three warps)
     kv_copy_role<NP, NSLOT, C::PANEL_LOG, PAGED, WIN>(a, &tm_k, &tm_v, g, kt0, n,
@@ -1018,8 +1054,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Type of an output row: fp32, or rounded once to f16 or bf16.
+constexpr int kOutF32 = 0, kOutF16 = 1, kOutBf16 = 2;
+
 #include "prefill_pair.cuh"
 #include "decode_kernel.cuh"
+#include "decode_stream.cuh"
 #include "kv_append.cuh"
 #include "step_tables.cuh"
 #include "qk_rope.cuh"
@@ -1033,9 +1073,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // before the weights are known: one memory latency per four parts, not one per part and pass.
 // Every lane takes part in every shuffle (at D = 64 only lanes 0-15 own columns, but the
 // weights of parts 16-31 sit in lanes 16-31).
-// OUT: the row's type at dst, fp32 or (rounded once) f16 or bf16.
-constexpr int kOutF32 = 0, kOutF16 = 1, kOutBf16 = 2;
-
+// OUT: the row's type at dst.
 template <int NPASS, int OUT>  // 128-column passes: 1 for D = 64 and 128, 2 for D = 256
 __device__ __forceinline__ void merge_row(const float* __restrict__ o, int64_t o_stride,
                                           const float* __restrict__ lse_p, int64_t lse_stride,
@@ -1241,10 +1279,10 @@ bool make_q_map(CUtensorMap* map, const void* base, bool bf16, int D, int G, int
   return r == CUDA_SUCCESS;
 }
 
-template <int D, bool PAGED, bool BF16, bool SQ = false, bool WIN = false>
+template <int D, bool PAGED, bool BF16, bool SQ = false, bool WIN = false, bool PRE = false>
 cudaError_t launch_prefill(int64_t grid, cudaStream_t st, const CUtensorMap& tk,
                            const CUtensorMap& tv, const PrefillArgs& a, const ItemTable& it) {
-  auto kern = prefill_kernel<D, PAGED, BF16, SQ, WIN>;
+  auto kern = prefill_kernel<D, PAGED, BF16, SQ, WIN, PRE>;
   static std::atomic<uint64_t> configured{0};  // one bit per device ordinal
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1260,11 +1298,11 @@ cudaError_t launch_prefill(int64_t grid, cudaStream_t st, const CUtensorMap& tk,
   return cudaGetLastError();
 }
 
-template <bool PAGED, bool BF16, bool WIN = false>
+template <bool PAGED, bool BF16, bool WIN = false, bool PRE = false>
 cudaError_t launch_pair(int64_t grid, cudaStream_t st, const CUtensorMap& tk,
                         const CUtensorMap& tv, const CUtensorMap& tq, const PrefillArgs& a,
                         const ItemTable& it) {
-  auto kern = prefill_pair_kernel<PAGED, BF16, WIN>;
+  auto kern = prefill_pair_kernel<PAGED, BF16, WIN, PRE>;
   static std::atomic<uint64_t> configured{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1332,9 +1370,9 @@ cudaError_t launch_decode(int64_t grid, cudaStream_t st, const CUtensorMap& tk,
     decode_batch_kernel<D, BF16, WIN><<<(unsigned)grid, kThreads, DecCfg<D>::LAUNCH_SMEM, st>>>(
         tk, tv, a, it);
   } else {
-    e = configure_decode(decode_kernel<D, BF16, WIN>, DecCfg<D>::LAUNCH_SMEM, configured);
+    e = configure_decode(decode_kernel<D, BF16>, DecCfg<D>::LAUNCH_SMEM, configured);
     if (e != cudaSuccess) return e;
-    decode_kernel<D, BF16, WIN><<<(unsigned)grid, kThreads, DecCfg<D>::LAUNCH_SMEM, st>>>(tk, tv, a);
+    decode_kernel<D, BF16><<<(unsigned)grid, kThreads, DecCfg<D>::LAUNCH_SMEM, st>>>(tk, tv, a);
   }
   return cudaGetLastError();
 }
@@ -1347,6 +1385,46 @@ cudaError_t launch_decode_d(int D, bool bf16, int64_t grid, cudaStream_t st,
                           : launch_decode<128, false, BAL, WIN>(grid, st, tk, tv, a, it))
                   : (bf16 ? launch_decode<256, true, BAL, WIN>(grid, st, tk, tv, a, it)
                           : launch_decode<256, false, BAL, WIN>(grid, st, tk, tv, a, it));
+}
+
+// The stream kernel on `ctas` CTAs, then its merge (programmatic launch: the merge's launch
+// overlaps the stream kernel's end). a.ws_o / ws_lse: the rows of the stream kernel's partials.
+// PREFIX: every unit leaves a partial, and n_pre partials of the prefix join (see the kernels).
+template <int D, bool BF16, bool PREFIX>
+cudaError_t launch_stream(int64_t ctas, cudaStream_t st, const CUtensorMap& tk,
+                          const CUtensorMap& tv, const PrefillArgs& a, const float* pre_o,
+                          const float* pre_lse, int n_pre) {
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = configure_decode(decode_stream_kernel<D, BF16, !PREFIX>,
+                                   StreamCfg<D>::LAUNCH_SMEM, configured);
+  if (e != cudaSuccess) return e;
+  decode_stream_kernel<D, BF16, !PREFIX>
+      <<<(unsigned)ctas, kThreads, StreamCfg<D>::LAUNCH_SMEM, st>>>(tk, tv, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = ceil_div64((int64_t)a.batch * a.Hq, kStreamRuns / 32);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(blocks, 4 * 148), 1, 1);
+  cfg.blockDim = dim3(kStreamRuns, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, merge_stream_kernel<D, BF16 ? kOutBf16 : kOutF16, PREFIX>, a,
+                            ctas, pre_o, pre_lse, n_pre);
+}
+
+template <bool PREFIX>
+cudaError_t launch_stream_d(int D, bool bf16, int64_t ctas, cudaStream_t st, const CUtensorMap& tk,
+                            const CUtensorMap& tv, const PrefillArgs& a, const float* pre_o,
+                            const float* pre_lse, int n_pre) {
+  if (D == 128)
+    return bf16 ? launch_stream<128, true, PREFIX>(ctas, st, tk, tv, a, pre_o, pre_lse, n_pre)
+                : launch_stream<128, false, PREFIX>(ctas, st, tk, tv, a, pre_o, pre_lse, n_pre);
+  return bf16 ? launch_stream<256, true, PREFIX>(ctas, st, tk, tv, a, pre_o, pre_lse, n_pre)
+              : launch_stream<256, false, PREFIX>(ctas, st, tk, tv, a, pre_o, pre_lse, n_pre);
 }
 
 // Paged single-CTA launches of decode and batches (sq: every Q tile holds <= 8 packed rows).
@@ -1498,48 +1576,40 @@ extern "C" int pa_prefill(const pa_plan_t* plan, const void* q, const void* k_po
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-// pa_decode (out fp32), and pa_window_decode's attention with a window (out of the input type).
-static int run_decode(const pa_plan_t* plan, const Window* win, const void* q,
-                      const void* k_pool, const void* v_pool, const int32_t* block_table,
-                      int table_stride, const int32_t* seq_lens, int64_t num_pages, float* out,
-                      float* lse_ws, uint64_t ws_bytes, pa_stream_t stream) {
-  if (!plan || plan->batch <= 0 || plan->chunk_rows != plan->batch || plan->q_tiles != 1 ||
-      plan->policy == PA_POLICY_BALANCED ||  // batch plans run through pa_batch_prefill
-      plan->policy == PA_POLICY_WINDOW || (plan->policy == PA_POLICY_WINDOW_DECODE) != !!win)
-    return PA_ERR_INVALID_ARG;
+namespace pa {
+// Checks of the arguments that every decode entry point takes, its tensor maps (pages of K, V boxes
+// over all of D) and its kernel arguments but for the workspace.
+static int decode_args(const pa_plan_t* plan, const void* q, const void* k_pool,
+                       const void* v_pool, const int32_t* block_table, int table_stride,
+                       const int32_t* seq_lens, int64_t num_pages, void* out, CUtensorMap* tk,
+                       CUtensorMap* tv, PrefillArgs* args) {
   if (!q || !k_pool || !v_pool || !block_table || !seq_lens || !out || table_stride <= 0 ||
       num_pages <= 0)
     return PA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
     return PA_ERR_INVALID_ARG;
-  const int D = plan->head_dim, S = plan->splits, B = plan->batch, PS = plan->page_size;
+  const int D = plan->head_dim, B = plan->batch, PS = plan->page_size;
   if (D != 64 && D != 128 && D != 256) return PA_ERR_UNSUPPORTED;
-  if (S < 1 || S > PA_MAX_SPLITS || plan->n_q_heads != plan->n_kv_heads * plan->group ||
-      plan->group > kTileRows || plan->units != (int64_t)B * plan->n_kv_heads * S)
+  if (plan->n_q_heads != plan->n_kv_heads * plan->group || plan->group > kTileRows)
     return PA_ERR_INVALID_ARG;
-  if (S > 1 && (!lse_ws || !aligned16(lse_ws) || ws_bytes < plan->ws_bytes))
-    return PA_ERR_WORKSPACE;
   if (num_pages * PS + kTileKeys >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
   const bool bf16 = plan->dtype == PA_BF16;
   const int64_t rows = num_pages * PS;
   const int v_rows = std::min(PS, 128 / (D / 64));
-  CUtensorMap tk, tv;
-  if (!make_k_map(&tk, k_pool, bf16, D, plan->n_kv_heads, rows, PS) ||
-      !make_v_map(&tv, v_pool, bf16, D, plan->n_kv_heads, rows, v_rows, D / 64))
+  if (!make_k_map(tk, k_pool, bf16, D, plan->n_kv_heads, rows, PS) ||
+      !make_v_map(tv, v_pool, bf16, D, plan->n_kv_heads, rows, v_rows, D / 64))
     return PA_ERR_CUDA;
-  PrefillArgs a;
+  PrefillArgs& a = *args;
   memset(&a, 0, sizeof a);
   a.q = static_cast<const uint16_t*>(q);
   a.page_table = block_table;
-  a.out = out;
-  a.ws_o = S > 1 ? lse_ws : nullptr;
-  a.ws_lse = S > 1 ? lse_ws + (int64_t)S * B * plan->n_q_heads * D : nullptr;
+  a.out = static_cast<float*>(out);
   a.R = 1;
   a.Hq = plan->n_q_heads;
   a.Hkv = plan->n_kv_heads;
   a.G = plan->group;
   a.q_tiles = 1;
-  a.splits = S;
+  a.splits = 1;
   a.page_rows = PS;
   a.page_shift = __builtin_ctz((unsigned)PS);
   a.pages_per_tile = kTileKeys / PS;
@@ -1555,31 +1625,54 @@ static int run_decode(const pa_plan_t* plan, const Window* win, const void* q,
   a.batch = B;
   a.table_stride = table_stride;
   a.seq_lens = seq_lens;
-  if (win) {
-    a.window = win->window;
-    a.sinks = win->sinks;
-  }
-  thread_local ItemTable table;  // unused by decode units
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int64_t grid = plan->units;
-  if (grid >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
-  cudaError_t e;
-  if (decode_swapped(D, plan->group))
-    e = win ? launch_decode_d<false, true>(D, bf16, grid, st, tk, tv, a, table)
-            : launch_decode_d<false>(D, bf16, grid, st, tk, tv, a, table);
-  else
-    e = win ? launch_paged_single<true>(D, bf16, plan->group <= 8, grid, st, tk, tv, a, table)
-            : launch_paged_single(D, bf16, plan->group <= 8, grid, st, tk, tv, a, table);
-  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return PA_OK;
 }
+}  // namespace pa
 
 extern "C" int pa_decode(const pa_plan_t* plan, const void* q, const void* k_pool,
                          const void* v_pool, const int32_t* block_table, int table_stride,
                          const int32_t* seq_lens, int64_t num_pages, float* out, float* lse_ws,
                          uint64_t ws_bytes, pa_stream_t stream) {
-  return run_decode(plan, nullptr, q, k_pool, v_pool, block_table, table_stride, seq_lens,
-                    num_pages, out, lse_ws, ws_bytes, stream);
+  if (!plan || plan->batch <= 0 || plan->chunk_rows != plan->batch || plan->q_tiles != 1 ||
+      plan->policy == PA_POLICY_BALANCED ||  // batch plans run through pa_batch_prefill
+      plan->policy >= PA_POLICY_WINDOW)      // and these through entry points of their own
+    return PA_ERR_INVALID_ARG;
+  const int D = plan->head_dim, S = plan->splits, B = plan->batch;
+  if (S < 1 || S > PA_MAX_SPLITS || plan->units != (int64_t)B * plan->n_kv_heads * S)
+    return PA_ERR_INVALID_ARG;
+  if (S > 1 && (!lse_ws || !aligned16(lse_ws) || ws_bytes < plan->ws_bytes))
+    return PA_ERR_WORKSPACE;
+  CUtensorMap tk, tv;
+  PrefillArgs a;
+  const int st = decode_args(plan, q, k_pool, v_pool, block_table, table_stride, seq_lens,
+                             num_pages, out, &tk, &tv, &a);
+  if (st != PA_OK) return st;
+  const bool bf16 = plan->dtype == PA_BF16;
+  a.splits = S;
+  a.ws_o = S > 1 ? lse_ws : nullptr;
+  a.ws_lse = S > 1 ? lse_ws + (int64_t)S * B * plan->n_q_heads * D : nullptr;
+  thread_local ItemTable table;  // unused by decode units
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t grid = plan->units;
+  if (grid >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
+  cudaError_t e;
+  if (decode_swapped(D, plan->group))
+    e = launch_decode_d<false>(D, bf16, grid, cs, tk, tv, a, table);
+  else
+    e = launch_paged_single(D, bf16, plan->group <= 8, grid, cs, tk, tv, a, table);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
+
+namespace pa {
+// Merge of S uniform partials into 16-bit rows.
+static int merge_rows16(const float* ws_o, const float* ws_lse, void* out, int S, int64_t rows,
+                        int D, bool bf16, cudaStream_t st) {
+  auto merge = bf16 ? combine_kernel<kOutBf16> : combine_kernel<kOutF16>;
+  merge<<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(ws_o, ws_lse, static_cast<float*>(out), S,
+                                                    rows, D);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+}  // namespace pa
 
 extern "C" int pa_window_decode(const pa_plan_t* plan, int window, int n_sinks, const void* q,
                                 const void* k_pool, const void* v_pool,
@@ -1587,24 +1680,135 @@ extern "C" int pa_window_decode(const pa_plan_t* plan, int window, int n_sinks, 
                                 const int32_t* seq_lens, int64_t num_pages, void* out,
                                 float* lse_ws, uint64_t ws_bytes, pa_stream_t stream) {
   if (window < 1 || n_sinks < 0) return PA_ERR_INVALID_ARG;
-  const Window win{window, n_sinks};
-  const int st = run_decode(plan, &win, q, k_pool, v_pool, block_table, table_stride, seq_lens,
-                            num_pages, static_cast<float*>(out), lse_ws, ws_bytes, stream);
-  if (st != PA_OK || plan->splits == 1) return st;
-  const int64_t RH = (int64_t)plan->batch * plan->n_q_heads;
-  const float* ws_lse = lse_ws + (int64_t)plan->splits * RH * plan->head_dim;
-  auto merge = plan->dtype == PA_BF16 ? combine_kernel<kOutBf16> : combine_kernel<kOutF16>;
-  merge<<<(unsigned)((RH + 7) / 8), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      lse_ws, ws_lse, static_cast<float*>(out), plan->splits, RH, plan->head_dim);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  if (!plan || plan->policy != PA_POLICY_WINDOW_DECODE || plan->batch <= 0 ||
+      plan->chunk_rows != plan->batch || plan->q_tiles != 1 || plan->n_kv_heads <= 0)
+    return PA_ERR_INVALID_ARG;
+  const int D = plan->head_dim, G = plan->group;
+  const int64_t rows = (int64_t)plan->batch * plan->n_q_heads;
+  const DecodeWork w = decode_work(plan->num_sms, D, G, plan->n_kv_heads, plan->batch,
+                                   window_most_tiles(plan->hist_len, window, n_sinks));
+  if (plan->units != w.units || plan->splits != w.splits || plan->ws_bytes != w.ws_bytes(D, G, rows))
+    return PA_ERR_INVALID_ARG;  // not this window's plan
+  if (plan->ws_bytes > 0 && (!lse_ws || !aligned16(lse_ws) || ws_bytes < plan->ws_bytes))
+    return PA_ERR_WORKSPACE;
+  CUtensorMap tk, tv;
+  PrefillArgs a;
+  const int st = decode_args(plan, q, k_pool, v_pool, block_table, table_stride, seq_lens,
+                             num_pages, out, &tk, &tv, &a);
+  if (st != PA_OK) return st;
+  const bool bf16 = plan->dtype == PA_BF16;
+  a.window = window;
+  a.sinks = n_sinks;
+  a.splits = w.splits;
+  a.ws_o = plan->ws_bytes > 0 ? lse_ws : nullptr;
+  a.ws_lse = plan->ws_bytes > 0 ? lse_ws + w.ws_rows(G, rows) * D : nullptr;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (w.stream) {
+    e = launch_stream_d<false>(D, bf16, w.units, cs, tk, tv, a, nullptr, nullptr, 0);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  }
+  thread_local ItemTable table;  // unused by decode units
+  e = launch_paged_single<true>(D, bf16, G <= 8, w.units, cs, tk, tv, a, table);
+  if (e != cudaSuccess) return PA_ERR_CUDA;
+  if (w.splits == 1) return PA_OK;
+  return merge_rows16(a.ws_o, a.ws_lse, out, w.splits, rows, D, bf16, cs);
 }
 
+extern "C" int pa_prefix_decode(const pa_plan_t* plan, int64_t prefix_len, const void* q,
+                                const void* k_pool, const void* v_pool,
+                                const int32_t* prefix_table, const int32_t* block_table,
+                                int table_stride, const int32_t* seq_lens, int64_t num_pages,
+                                void* out, float* lse_ws, uint64_t ws_bytes,
+                                pa_stream_t stream) {
+  if (!plan || plan->policy != PA_POLICY_PREFIX_DECODE || plan->batch <= 0 ||
+      plan->chunk_rows != plan->batch || plan->n_kv_heads <= 0 || prefix_len <= 0 ||
+      prefix_len % plan->page_size || !prefix_table)
+    return PA_ERR_INVALID_ARG;
+  const int D = plan->head_dim, G = plan->group, PS = plan->page_size, B = plan->batch;
+  const int64_t rows = (int64_t)B * plan->n_q_heads;
+  const PrefixWork w = prefix_work(plan->num_sms, D, G, plan->n_kv_heads, B, prefix_len,
+                                   plan->hist_len);
+  if (plan->units != w.own.units || plan->splits != w.splits || plan->ctas_per_unit != w.per ||
+      plan->q_tiles != w.q_tiles || plan->ws_bytes != w.ws_bytes(D, G, rows))
+    return PA_ERR_INVALID_ARG;  // not this prefix's plan
+  if (!lse_ws || !aligned16(lse_ws) || ws_bytes < plan->ws_bytes) return PA_ERR_WORKSPACE;
+  CUtensorMap tk, tv;
+  PrefillArgs a;
+  int st = decode_args(plan, q, k_pool, v_pool, block_table, table_stride, seq_lens, num_pages,
+                       out, &tk, &tv, &a);
+  if (st != PA_OK) return st;
+  const bool bf16 = plan->dtype == PA_BF16;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  float* const lse = lse_ws + w.ws_rows(G, rows) * D;
+
+  // The prefix: packed rows (sequence, head) against the shared pages, in uniform splits.
+  PrefillArgs p = a;
+  CUtensorMap pk = tk, pv = tv, pq;
+  memset(&pq, 0, sizeof pq);
+  const int64_t pool_rows = num_pages * PS;
+  if (w.per == 2) {  // the pair kernel's boxes and Q, as in pa_prefill
+    const int box = std::min(PS, 64);
+    p.k_rows = p.v_rows = box;
+    p.v_shift = __builtin_ctz((unsigned)box);
+    p.k_atoms = PS == 16 ? 1 : 0;
+    p.q_tma = kTileRows % G == 0 ? 1 : 0;
+    if (!(p.k_atoms ? make_v_map(&pk, k_pool, bf16, D, plan->n_kv_heads, pool_rows, 8, D / 64)
+                    : make_k_map(&pk, k_pool, bf16, D, plan->n_kv_heads, pool_rows, box)) ||
+        !make_v_map(&pv, v_pool, bf16, D, plan->n_kv_heads, pool_rows, box, 2) ||
+        (p.q_tma && !make_q_map(&pq, q, bf16, D, G, plan->n_kv_heads, B)))
+      return PA_ERR_CUDA;
+  }
+  p.page_table = prefix_table;
+  p.table_len = prefix_len / PS;
+  p.total_keys = prefix_len;
+  p.batch = 0;
+  p.R = B;
+  p.q_tiles = w.q_tiles;
+  p.splits = w.splits;
+  p.rows_per_block = w.per * kTileRows;
+  p.ws_o = lse_ws;
+  p.ws_lse = lse;
+  const int64_t grid =
+      ceil_div64(w.q_tiles, w.per) * plan->n_kv_heads * (int64_t)w.splits * w.per;
+  if (grid >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
+  thread_local ItemTable table;  // unused
+  cudaError_t e;
+  if (w.per == 2)
+    e = bf16 ? launch_pair<true, true, false, true>(grid, cs, pk, pv, pq, p, table)
+             : launch_pair<true, false, false, true>(grid, cs, pk, pv, pq, p, table);
+  else if (D == 64)
+    e = bf16 ? launch_prefill<64, true, true, false, false, true>(grid, cs, pk, pv, p, table)
+             : launch_prefill<64, true, false, false, false, true>(grid, cs, pk, pv, p, table);
+  else if (D == 128)
+    e = bf16 ? launch_prefill<128, true, true, false, false, true>(grid, cs, pk, pv, p, table)
+             : launch_prefill<128, true, false, false, false, true>(grid, cs, pk, pv, p, table);
+  else
+    e = bf16 ? launch_prefill<256, true, true, false, false, true>(grid, cs, pk, pv, p, table)
+             : launch_prefill<256, true, false, false, false, true>(grid, cs, pk, pv, p, table);
+  if (e != cudaSuccess) return PA_ERR_CUDA;
+
+  // Every sequence's own keys, from the prefix's end on, and the merge of all partials.
+  a.window = int64_t(1) << 40;
+  a.sinks = 0;
+  a.first_key = prefix_len;
+  a.ws_o = lse_ws + (int64_t)w.splits * rows * D;
+  a.ws_lse = lse + (int64_t)w.splits * rows;
+  if (w.own.stream) {
+    e = launch_stream_d<true>(D, bf16, w.own.units, cs, tk, tv, a, lse_ws, lse, w.splits);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  }
+  a.splits = w.own.splits;
+  e = launch_paged_single<true>(D, bf16, G <= 8, w.own.units, cs, tk, tv, a, table);
+  if (e != cudaSuccess) return PA_ERR_CUDA;
+  return merge_rows16(lse_ws, lse, out, w.splits + w.own.splits, rows, D, bf16, cs);
+}
 
 extern "C" int pa_combine(const pa_plan_t* plan, const float* lse_ws, uint64_t ws_bytes,
                           float* out, pa_stream_t stream) {
   if (!plan || (plan->policy == PA_POLICY_BALANCED && plan->batch != 0) ||
-      plan->policy == PA_POLICY_WINDOW || plan->policy == PA_POLICY_WINDOW_DECODE)
-    return PA_ERR_INVALID_ARG;  // batched plans merge with pa_batch_combine, windowed ones alone
+      plan->policy >= PA_POLICY_WINDOW)
+    return PA_ERR_INVALID_ARG;  // batched plans merge with pa_batch_combine, the last on their own
   const int S = plan->splits;
   if (plan->policy == PA_POLICY_BALANCED) {
     Schedule sch;
@@ -1932,22 +2136,21 @@ extern "C" int pa_block_tables(int batch, const int32_t* q_lens, const int32_t* 
 }
 
 namespace pa {
-template <int D, bool BF16, int NU>
-static void launch_qk_rope(unsigned blocks, cudaStream_t st, const RopeArgs& a, bool interleaved) {
-  if (interleaved)
-    qk_rope_append_kernel<D, BF16, true, NU><<<blocks, 256, 0, st>>>(a);
-  else
-    qk_rope_append_kernel<D, BF16, false, NU><<<blocks, 256, 0, st>>>(a);
-}
 template <int D, bool BF16>
 static int run_qk_rope(RopeArgs& a, bool interleaved, cudaStream_t st) {
   constexpr int HPW = 256 / D;  // heads of a warp's set
-  constexpr int NU = 4;
-  a.q_warps = (a.Hq + NU * HPW - 1) / (NU * HPW);
-  a.kv_warps = (2 * a.Hkv + NU * HPW - 1) / (NU * HPW);
+  // Sets a warp: as many as leave 32 warps an SM (a token's set-up is paid once a warp), one at
+  // least, and at most all of the token's query sets, or all of its key and value sets.
+  const int64_t q_sets = (a.Hq + HPW - 1) / HPW, kv_sets = (2 * a.Hkv + HPW - 1) / HPW;
+  const int64_t n = std::max<int64_t>(1, a.rows * (q_sets + kv_sets) / (148 * 32));
+  a.q_warps = (int)((q_sets + n - 1) / n);
+  a.kv_warps = (int)((kv_sets + n - 1) / n);
   const int64_t blocks = ((int64_t)a.rows * (a.q_warps + a.kv_warps) + 7) / 8;
-  if (blocks >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
-  launch_qk_rope<D, BF16, NU>((unsigned)blocks, st, a, interleaved);
+  if (blocks * 8 >= (int64_t(1) << 32)) return PA_ERR_UNSUPPORTED;
+  if (interleaved)
+    qk_rope_append_kernel<D, BF16, true><<<(unsigned)blocks, 256, 0, st>>>(a);
+  else
+    qk_rope_append_kernel<D, BF16, false><<<(unsigned)blocks, 256, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 }  // namespace pa

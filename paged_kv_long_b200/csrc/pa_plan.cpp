@@ -465,27 +465,124 @@ extern "C" int pa_window_plan(int num_sms, int n_q_heads, int n_kv_heads, int he
                     &win, dtype, scale, plan);
 }
 
-extern "C" int pa_window_decode_plan(int num_sms, int n_q_heads, int n_kv_heads, int head_dim,
-                                     int page_size, int batch, int64_t max_seq_len, int window,
-                                     int n_sinks, int dtype, float scale, int splits_override,
+namespace pa {
+
+int64_t window_most_tiles(int64_t max_len, int64_t window, int64_t sinks) {
+  return std::min(ceil_div64(max_len, kTileKeys),
+                  ceil_div64(sinks, kTileKeys) + ceil_div64(window - 1, kTileKeys) + 1);
+}
+
+DecodeWork decode_work(int num_sms, int D, int G, int Hkv, int64_t batch, int64_t tiles) {
+  DecodeWork w;
+  w.stream = decode_swapped(D, G);
+  const int64_t units = batch * Hkv;
+  if (w.stream) {  // every CTA slot, but no more than one per two of the units' tiles and starts
+    w.splits = 1;
+    w.units = std::max<int64_t>(1, std::min<int64_t>((int64_t)num_sms * kDecCtasPerSm,
+                                                     units * (tiles + 1) / 2));
+  } else {  // about two units per SM
+    w.splits = (int32_t)std::max<int64_t>(
+        1, std::min<int64_t>({ceil_div64(2 * (int64_t)num_sms, units), (int64_t)PA_MAX_SPLITS,
+                              tiles}));
+    w.units = units * w.splits;
+  }
+  return w;
+}
+
+PrefixWork prefix_work(int num_sms, int D, int G, int Hkv, int64_t batch, int64_t prefix_len,
+                       int64_t max_len) {
+  PrefixWork w;
+  const CostModel cm(D);
+  w.q_tiles = (int32_t)q_tiles_for(batch, G);
+  w.per = D == 256 && w.q_tiles > 1 ? 2 : 1;
+  const int64_t tiles = ceil_div64(prefix_len, kTileKeys);
+  const int64_t own_keys = std::max<int64_t>(1, max_len - prefix_len);
+  w.own = decode_work(num_sms, D, G, Hkv, batch,
+                      ceil_div64(own_keys, kTileKeys) + (prefix_len % kTileKeys ? 1 : 0));
+  if (!w.own.stream) {  // always partials (two splits at least), 32 with the prefix's in all
+    w.own.splits = std::min(8, std::max(2, w.own.splits));
+    w.own.units = batch * Hkv * w.own.splits;
+  }
+  // The split count with the shortest waves of units plus the merge's traffic.
+  const int64_t units = ceil_div64(w.q_tiles, w.per) * Hkv;
+  const int64_t slots = std::max(1, num_sms / w.per);
+  const int64_t most = std::min<int64_t>(tiles, w.own.stream ? 148 : PA_MAX_SPLITS - w.own.splits);
+  double best = 0.0;
+  w.splits = 1;
+  for (int64_t S = 1; S <= most; ++S) {
+    const double t = (double)ceil_div64(units * S, slots) *
+                         ((double)ceil_div64(tiles, S) * cm.tile_us + cm.unit_us) +
+                     2.0 * S * batch * G * Hkv * (D + 1) * 4.0 * cm.combine_us_per_byte;
+    if (S == 1 || t < best) {
+      best = t;
+      w.splits = (int32_t)S;
+    }
+  }
+  return w;
+}
+
+}  // namespace pa
+
+extern "C" int pa_prefix_decode_plan(int num_sms, int n_q_heads, int n_kv_heads, int head_dim,
+                                     int page_size, int batch, int64_t prefix_len,
+                                     int64_t max_seq_len, int dtype, float scale,
                                      pa_plan_t* plan) {
   if (!plan) return PA_ERR_INVALID_ARG;
   memset(plan, 0, sizeof *plan);
-  if (window < 1 || n_sinks < 0 || max_seq_len < 1) return PA_ERR_INVALID_ARG;
-  // the most tiles a sequence's window and sinks reach, whatever its length up to max_seq_len
-  const int64_t tiles =
-      std::min(pa::ceil_div64(max_seq_len, pa::kTileKeys),
-               pa::ceil_div64(n_sinks, pa::kTileKeys) + pa::ceil_div64(window - 1, pa::kTileKeys) +
-                   1);
+  // the checks and the shape's fields are a decode plan's
   const int st = pa_decode_plan(num_sms, n_q_heads, n_kv_heads, head_dim, page_size, batch,
-                                tiles * pa::kTileKeys, dtype, scale, splits_override, plan);
+                                std::max(prefix_len, max_seq_len), dtype, scale, 1, plan);
   if (st != PA_OK) return st;
-  if (max_seq_len + pa::kTileKeys >= (int64_t(1) << 31)) {
+  if (prefix_len <= 0 || max_seq_len < 1 || prefix_len % page_size) {
+    memset(plan, 0, sizeof *plan);
+    return PA_ERR_INVALID_ARG;
+  }
+  const pa::PrefixWork w = pa::prefix_work(num_sms, head_dim, plan->group, n_kv_heads, batch,
+                                           prefix_len, max_seq_len);
+  const int64_t rows = (int64_t)batch * n_q_heads;
+  if (w.own.units >= (int64_t(1) << 31) ||
+      pa::ceil_div64(w.q_tiles, w.per) * n_kv_heads * w.splits * w.per >= (int64_t(1) << 31)) {
     memset(plan, 0, sizeof *plan);
     return PA_ERR_UNSUPPORTED;
   }
-  plan->policy = PA_POLICY_WINDOW_DECODE;
+  const CostModel cm(head_dim);
+  plan->policy = PA_POLICY_PREFIX_DECODE;
   plan->hist_len = max_seq_len;
+  plan->q_tiles = w.q_tiles;
+  plan->ctas_per_unit = w.per;
+  plan->splits = w.splits;
+  plan->units = w.own.units;
+  plan->ws_bytes = w.ws_bytes(head_dim, plan->group, rows);
+  const double share = (double)w.q_tiles * n_kv_heads *
+                       pa::ceil_div64(prefix_len, pa::kTileKeys) / num_sms;
+  plan->est_us = (float)(2 * cm.unit_us + share * cm.tile_us + cm.combine_fixed_us);
+  return PA_OK;
+}
+
+extern "C" int pa_window_decode_plan(int num_sms, int n_q_heads, int n_kv_heads, int head_dim,
+                                     int page_size, int batch, int64_t max_seq_len, int window,
+                                     int n_sinks, int dtype, float scale, pa_plan_t* plan) {
+  if (!plan) return PA_ERR_INVALID_ARG;
+  memset(plan, 0, sizeof *plan);
+  if (window < 1 || n_sinks < 0) return PA_ERR_INVALID_ARG;
+  // the checks and the shape's fields are a decode plan's
+  const int st = pa_decode_plan(num_sms, n_q_heads, n_kv_heads, head_dim, page_size, batch,
+                                max_seq_len, dtype, scale, 1, plan);
+  if (st != PA_OK) return st;
+  const int64_t tiles = pa::window_most_tiles(max_seq_len, window, n_sinks);
+  const pa::DecodeWork w =
+      pa::decode_work(num_sms, head_dim, plan->group, n_kv_heads, batch, tiles);
+  if (w.units >= (int64_t(1) << 31)) {
+    memset(plan, 0, sizeof *plan);
+    return PA_ERR_UNSUPPORTED;
+  }
+  const CostModel cm(head_dim);
+  plan->policy = PA_POLICY_WINDOW_DECODE;
+  plan->splits = w.splits;
+  plan->units = w.units;
+  plan->ws_bytes = w.ws_bytes(head_dim, plan->group, (int64_t)batch * n_q_heads);
+  const double share = (double)batch * n_kv_heads * tiles / num_sms;
+  plan->est_us = (float)(cm.unit_us + share * cm.tile_us);
   return PA_OK;
 }
 

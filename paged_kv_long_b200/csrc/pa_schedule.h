@@ -44,4 +44,42 @@ struct Window {
 bool build_batch(int num_sms, int head_dim, int per, int G, int Hkv, const Batch& bt,
                  Schedule* out, const Window* win = nullptr);
 
+// Most KV tiles that a window and sinks reach in a sequence of up to max_len keys.
+int64_t window_most_tiles(int64_t max_len, int64_t window, int64_t sinks);
+
+// How the decode entry points with a 16-bit output share their (sequence, KV head) units, of up
+// to `tiles` KV tiles each: groups of up to 8 heads at head dim 128 or 256 on the stream kernel
+// (`units` CTAs, equal shares of the tiles, two part slots of G rows each), the others in uniform
+// splits of the single-CTA kernel (`units` = batch * Hkv * splits).
+struct DecodeWork {
+  bool stream;
+  int32_t splits;
+  int64_t units;
+  // Workspace rows (D + 1 fp32 each) of the partials; `rows` = batch * Hq output rows.
+  int64_t ws_rows(int G, int64_t rows) const {
+    return stream ? 2 * units * G : splits > 1 ? splits * rows : 0;
+  }
+  uint64_t ws_bytes(int D, int G, int64_t rows) const {
+    return (uint64_t)ws_rows(G, rows) * (D + 1) * 4ull;
+  }
+};
+DecodeWork decode_work(int num_sms, int D, int G, int Hkv, int64_t batch, int64_t tiles);
+
+// A decode step over a shared prefix: the prefix's packed (sequence, head) rows in `q_tiles` tiles
+// a KV head, on `per` CTAs a unit, `splits` uniform splits of its keys; the sequences' own keys as
+// decode_work shares them. Workspace rows: the prefix's partials [splits][rows], then the own
+// part's: [rows] of whole units and the part slots (stream kernel), or its uniform partials.
+struct PrefixWork {
+  int32_t per, q_tiles, splits;
+  DecodeWork own;
+  int64_t ws_rows(int G, int64_t rows) const {
+    return splits * rows + (own.stream ? rows : 0) + own.ws_rows(G, rows);
+  }
+  uint64_t ws_bytes(int D, int G, int64_t rows) const {
+    return (uint64_t)ws_rows(G, rows) * (D + 1) * 4ull;
+  }
+};
+PrefixWork prefix_work(int num_sms, int D, int G, int Hkv, int64_t batch, int64_t prefix_len,
+                       int64_t max_len);
+
 }  // namespace pa

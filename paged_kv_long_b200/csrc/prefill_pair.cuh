@@ -92,7 +92,7 @@ struct PairSync {
 
 // Softmax + epilogue warps of the pair kernel (warps 0-3, one thread per packed Q row of this
 // CTA's tile = tensor-memory lane).
-template <bool PAGED, bool BF16, bool WIN, class VTail>
+template <bool PAGED, bool BF16, bool WIN, bool PRE, class VTail>
 __device__ __forceinline__ void softmax_pair_role(const PrefillArgs& a, const SoftmaxCtx& x,
                                                   const PairSync& y, VTail&& v_tail) {
   constexpr int D = 256;
@@ -133,7 +133,7 @@ __device__ __forceinline__ void softmax_pair_role(const PrefillArgs& a, const So
     }
   }
 
-  const int64_t limit = valid ? a.hist_len + tok : -1;  // last key this row may see
+  const int64_t limit = valid ? row_limit<PRE>(a, tok) : -1;  // last key this row may see
   const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
   float m_run = -INFINITY;  // running max of scale*log2(e)*score
   float l_run = 0.f;        // running sum of the probabilities (fp32)
@@ -263,11 +263,11 @@ __device__ __forceinline__ void softmax_pair_role(const PrefillArgs& a, const So
   if (ok) ok = wait_pv(n - 1);
   if (ok) {
     tc_fence_after();
-    write_row<D, WIN, BF16>(a, x, r, valid, tok, head, m_run, l_run, t_lane);
+    write_row<D, WIN, PRE, BF16>(a, x, r, valid, tok, head, m_run, l_run, t_lane);
   }
 }
 
-template <bool PAGED, bool BF16, bool WIN>
+template <bool PAGED, bool BF16, bool WIN, bool PRE>
 __global__ void __launch_bounds__(kPairThreads, 1)
     prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v,
@@ -301,7 +301,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else {
     unit_coords(blockIdx.x >> 1, (a.q_tiles + 1) / 2, a.Hkv, a.splits, &tp, &g, &s);
     const int64_t qt_last = 2 * tp + 1 < a.q_tiles ? 2 * tp + 1 : a.q_tiles - 1;
-    split_range(tile_kv_tiles(qt_last, a.R, a.G, a.hist_len), s, a.splits, &kt0, &kt1);
+    split_range(PRE ? ceil_div64(a.total_keys, kTileKeys)
+                    : tile_kv_tiles(qt_last, a.R, a.G, a.hist_len),
+                s, a.splits, &kt0, &kt1);
   }
   const int64_t qt = 2 * tp + rank;
   const int n = (int)(kt1 - kt0);
@@ -444,7 +446,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       }
       return true;
     };
-    softmax_pair_role<PAGED, BF16, WIN>(a, sc, ps, v_tail);
+    softmax_pair_role<PAGED, BF16, WIN, PRE>(a, sc, ps, v_tail);
   } else if (warp > kMmaWarp && warp < kPairPvWarp) {
     // ============================================================ TMA issuers (two warps)
     // Warp 5 fills the K ring (K(0), K(1), ... in tile order), warp 6 the V ring; lanes issue

@@ -143,7 +143,7 @@ def run_prefill(c, num_sms=None):
     return wp, got
 
 
-def run_decode(c, splits=0):
+def run_decode(c, num_sms=148):
     """Rows with no key are in the batch as length 0 (c.rows[b] == 0)."""
     import torch
     bd = _binding()
@@ -151,7 +151,7 @@ def run_decode(c, splits=0):
     B = len(c.rows)
     lens = np.array([h + r if r else 0 for r, h in zip(c.rows, c.hist)], np.int32)
     wp = bd.window_decode_plan(c.Hq, c.Hkv, c.D, c.PS, B, max(1, int(lens.max())), c.window,
-                               c.sinks, c.dtype, splits=splits)
+                               c.sinks, c.dtype, num_sms=num_sms)
     _, k, v, t = c.device()
     full = torch.zeros(B, c.Hq, c.D, dtype=c.dt)
     live = torch.from_numpy(lens > 0)
@@ -250,18 +250,26 @@ def test_plan_items_cover_the_visible_tiles_once(seed):
     assert p.ws_bytes == len(slots) * p.ctas_per_unit * 128 * (D + 1) * 4
 
 
-def test_decode_plan_splits_by_visible_tiles():
+def test_decode_plan_shares_the_visible_tiles():
     bd = _binding()
     mk = lambda **a: bd.window_decode_plan(**{**dict(  # noqa: E731
         n_q_heads=16, n_kv_heads=2, head_dim=256, page_size=16, batch=1, max_seq_len=32768,
         window=1000, n_sinks=4, dtype="f16", num_sms=148), **a}).plan
-    assert mk().splits == 10                  # 1 sink tile + 8 + 1
-    assert mk(n_sinks=0, window=1).splits == 1 and mk(n_sinks=0, window=129).splits == 2
-    assert mk(max_seq_len=100).splits == 1
-    p = mk(splits=7)
-    assert p.splits == 7 and p.hist_len == 32768 and p.policy == 5
-    assert p.ws_bytes == 7 * 16 * 257 * 4 and p.units == 14
-    assert mk(window=2**40).splits == 32     # a window past 2^31 sees every key anyway
+    # G 8 at D 256: CTAs that share the tiles (1 sink tile + 8 + 1, two heads) and the units'
+    # starts, two each at least
+    p = mk()
+    assert p.units == 11 and p.splits == 1 and p.hist_len == 32768 and p.policy == 5
+    assert p.ws_bytes == 11 * 2 * 8 * 257 * 4
+    assert mk(n_sinks=0, window=1).units == 2 and mk(n_sinks=0, window=129).units == 3
+    assert mk(max_seq_len=100).units == 2 and mk(batch=64).units == 296
+    assert mk(batch=64, num_sms=5).units == 10
+    assert mk(window=2**40).units == 257     # a window past 2^31 sees every key anyway
+    # G 16: uniform splits of the single-CTA kernel
+    p = mk(n_q_heads=32)
+    assert p.splits == 10 and p.units == 20 and p.ws_bytes == 10 * 32 * 257 * 4
+    assert mk(n_q_heads=32, batch=200).splits == 1 and mk(n_q_heads=32, batch=200).ws_bytes == 0
+    p = mk(head_dim=64, batch=3, window=10**6)
+    assert p.splits == 32 and p.units == 3 * 2 * 32
 
 
 def test_refusals():
@@ -282,10 +290,10 @@ def test_refusals():
         148, 4, 2, 64, 16, 1, ql.ctypes.data, hl.ctypes.data, w, s, 0, 0.0, ctypes.byref(p)))
     assert raw(0, 0) == raw(1, -1) == "PA_ERR_INVALID_ARG" and raw(1, 0) == "PA_OK"
     raw = lambda w, s: name(lib.pa_window_decode_plan(  # noqa: E731
-        148, 4, 2, 64, 16, 1, 9, w, s, 0, 0.0, 0, ctypes.byref(p)))
+        148, 4, 2, 64, 16, 1, 9, w, s, 0, 0.0, ctypes.byref(p)))
     assert raw(0, 0) == raw(1, -1) == "PA_ERR_INVALID_ARG" and raw(1, 0) == "PA_OK"
     for bad in (dict(head_dim=96), dict(page_size=24), dict(n_q_heads=5), dict(batch=0),
-                dict(max_seq_len=0), dict(max_seq_len=2**31), dict(splits=33)):
+                dict(max_seq_len=0), dict(max_seq_len=2**31)):
         with pytest.raises(bd.PaError):
             bd.window_decode_plan(**{**dict(n_q_heads=4, n_kv_heads=2, head_dim=64, page_size=16,
                                             batch=1, max_seq_len=9, window=4, num_sms=148), **bad})
@@ -322,6 +330,7 @@ def test_refusals():
                                None)) == bad
     # arguments
     assert decode(wd.plan, w=0) == decode(wd.plan, s=-1) == decode(wd.plan, q=None) == bad
+    assert decode(wd.plan, w=900) == bad      # another window: its tiles, CTAs and workspace
     assert decode(wd.plan, lens=None) == decode(wd.plan, out=None) == decode(wd.plan, table=None)
     assert decode(wd.plan, stride=0) == decode(wd.plan, pages=0) == bad
     assert decode(wd.plan, ws=None) == decode(wd.plan, n=16) == "PA_ERR_WORKSPACE"
@@ -347,20 +356,20 @@ def test_binding_refuses_the_other_plan():
 # ------------------------------------------------------------------------------------ GPU
 
 DECODE = [
-    # lens, window, sinks, Hq, Hkv, D, PS, dtype, splits
-    ([1], 1, 0, 8, 1, 256, 16, "f16", 0),
-    ([1, 2, 16, 17], 1, 1, 16, 2, 128, 16, "bf16", 0),
+    # lens, window, sinks, Hq, Hkv, D, PS, dtype, num_sms
+    ([1], 1, 0, 8, 1, 256, 16, "f16", 148),
+    ([1, 2, 16, 17], 1, 1, 16, 2, 128, 16, "bf16", 148),
     ([700, 0, 129, 128, 127], 128, 0, 16, 2, 256, 16, "f16", 1),
-    ([700, 0, 129, 256, 385, 1], 129, 4, 16, 2, 256, 64, "bf16", 0),
+    ([700, 0, 129, 256, 385, 1], 129, 4, 16, 2, 256, 64, "bf16", 148),
     ([2000, 1999, 1, 300], 500, 130, 24, 4, 256, 128, "bf16", 3),   # sinks over two tiles
-    ([5000, 40, 1024, 1025], 1000, 4, 32, 8, 128, 32, "f16", 0),
-    ([900, 901, 902], 10**6, 0, 8, 8, 128, 16, "f16", 0),           # the whole sequence
-    ([900, 901, 902], 300, 10**6, 8, 8, 128, 16, "f16", 0),
-    ([3000, 5, 129], 257, 20, 32, 2, 64, 16, "bf16", 0),            # G 16: single-CTA kernel
+    ([5000, 40, 1024, 1025], 1000, 4, 32, 8, 128, 32, "f16", 148),
+    ([900, 901, 902], 10**6, 0, 8, 8, 128, 16, "f16", 148),           # the whole sequence
+    ([900, 901, 902], 300, 10**6, 8, 8, 128, 16, "f16", 148),
+    ([3000, 5, 129], 257, 20, 32, 2, 64, 16, "bf16", 148),            # G 16: single-CTA kernel
     ([3000, 0, 5], 64, 300, 4, 4, 64, 128, "f16", 2),
-    ([4000, 3], 130, 1, 32, 2, 256, 16, "f16", 0),                  # G 16 at D 256
-    ([9000, 8999], 8000, 4, 8, 1, 256, 16, "f16", 32),
-    ([1500], 1000, 300, 8, 1, 128, 64, "bf16", 32),                 # more splits than tiles
+    ([4000, 3], 130, 1, 32, 2, 256, 16, "f16", 148),                  # G 16 at D 256
+    ([9000, 8999], 8000, 4, 8, 1, 256, 16, "f16", 100),
+    ([1500], 1000, 300, 8, 1, 128, 64, "bf16", 2),                  # four CTAs
     ([1500, 77], 1100, 300, 8, 1, 64, 64, "bf16", 1),               # one unit over both runs
 ]
 
@@ -368,11 +377,28 @@ DECODE = [
 @_gpu
 @pytest.mark.parametrize("i", range(len(DECODE)))
 def test_gpu_window_decode(i):
-    lens, w, s, Hq, Hkv, D, PS, dtype, splits = DECODE[i]
+    lens, w, s, Hq, Hkv, D, PS, dtype, sms = DECODE[i]
     c = Case(100 + i, [min(1, n) for n in lens], [max(0, n - 1) for n in lens], w, s, Hq, Hkv, D,
              PS, dtype)
-    wp, got = run_decode(c, splits)
-    c.check(got, what=f"S={wp.plan.splits}")
+    wp, got = run_decode(c, sms)
+    c.check(got, what=f"{wp.plan.units} units")
+
+
+@_gpu
+@pytest.mark.parametrize("D,Hq,Hkv,B", [(128, 16, 2, 300), (256, 8, 1, 257), (128, 3, 3, 700),
+                                        (64, 4, 2, 300)])
+@pytest.mark.parametrize("sms", [148, 7])
+def test_gpu_window_decode_large_batches(D, Hq, Hkv, B, sms):
+    """More sequences than the scan has runs, many of them empty: CTAs' shares begin and end
+    anywhere (several sequences inside one share, shares inside one sequence)."""
+    rng = np.random.default_rng(B + sms)
+    lens = rng.integers(0, 700, B)
+    lens[rng.random(B) < 0.3] = 0
+    lens[:3], lens[-2:] = 0, 0
+    lens[5] = 20000
+    c = Case(B, np.minimum(lens, 1), np.maximum(lens - 1, 0), 10000, 5, Hq, Hkv, D, 16, "f16")
+    _, got = run_decode(c, sms)
+    c.check(got)
 
 
 @_gpu
@@ -455,7 +481,7 @@ def test_gpu_window_fuzz(seed):
         rows = np.ones(B, int)
         rows[1:] = rng.integers(0, 2, B - 1)
         c = Case(seed, rows, hist, window, sinks, Hkv * G, Hkv, D, PS, dtype)
-        c.check(run_decode(c, int(rng.choice([0, 1, 2, 5])))[1])
+        c.check(run_decode(c, int(rng.choice([148, 1, 2, 5])))[1])
     else:
         rows = rng.integers(0, 200, B)
         rows[0] = max(1, rows[0])
@@ -468,7 +494,7 @@ def test_gpu_window_fuzz(seed):
 @_gpu
 def test_gpu_repeated_runs_and_full_windows_agree_with_the_framework():
     """Bit for bit the same on a second run; a window of the whole sequence equals pa_batch_prefill
-    and pa_decode rounded to the type (one row block each, uncut: the same arithmetic)."""
+    and pa_decode rounded to the type (units in one piece each: the same arithmetic)."""
     import torch
     bd = _binding()
     c = Case(7, [33, 1], [100, 300], 10**6, 0, 8, 2, 128, 16, "f16")
@@ -481,11 +507,13 @@ def test_gpu_repeated_runs_and_full_windows_agree_with_the_framework():
     if bp.plan.ws_bytes == 0:
         assert torch.equal(a, want.half())
     c = Case(8, [1, 1], [100, 300], 10**6, 0, 8, 2, 128, 16, "f16")
-    _, a = run_decode(c, splits=1)
+    _, a = run_decode(c)
+    assert torch.equal(a, run_decode(c)[1])
     q, k, v, t = c.device()
     dp = bd.decode_plan(8, 2, 128, 16, 2, 301, "f16", splits=1)
     want = bd.decode(dp, q, k, v, t, torch.tensor([101, 301], dtype=torch.int32, device="cuda"))
-    assert torch.equal(a, want.half().cpu())
+    # the parts of cut units join in fp32: equal up to the one rounding
+    assert (a - want.half().cpu()).abs().max() <= 2 * torch.finfo(torch.float16).eps * a.abs().max()
 
 
 @_gpu
