@@ -301,7 +301,9 @@ int pa_batch_combine(const pa_plan_t* plan, const int32_t* q_lens, const int64_t
  * pa_window_plan / pa_window_prefill — several sequences in one launch, each a chunk of q_lens[b]
  * rows after hist_lens[b] keys: arguments, limits and layouts of pa_batch_plan and
  * pa_batch_prefill, with the window, the sinks and the output's type. pa_window_prefill also
- * merges the parts of cut row blocks (there is no separate combine). A single piece is a batch of
+ * merges the parts of cut row blocks (there is no separate combine). A row block is two Q tiles at
+ * every head dim (ctas_per_unit = 2: a CTA pair at 256, one CTA of two tiles at 64 and 128) as soon
+ * as some sequence has two, else one. A single piece is a batch of
  * one, a decode step with host lengths a batch of one-row chunks. The plan's policy is
  * PA_POLICY_WINDOW, and `window`, `n_sinks` and the arrays must be those it was made with; other
  * entry points refuse the plan. pa_window_schedule_items lists its items: kt0 and kt1 count along

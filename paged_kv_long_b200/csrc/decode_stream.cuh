@@ -255,7 +255,8 @@ __device__ __forceinline__ void stream_copy_role(const PrefillArgs& a0, const CU
 }
 
 // WHOLE: the result of a whole unit is the output (16-bit); else a partial too (its row and LSE at
-// row b Hq + head of the workspace's first batch * Hq rows, before the part slots).
+// row b Hq + head of the workspace's first batch * Hq rows, before the part slots), and the
+// kernel is launched while the prefix's kernel before it ends.
 template <int D, bool BF16, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
     decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -305,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
   const StreamShare share(run[kStreamRuns], gridDim.x);
   if (blockIdx.x >= share.C) {
     if (warp == kMmaWarp) tmem_dealloc(tmem, kDecTmemCols);
+    if constexpr (!WHOLE) wait_dependencies();
     return;
   }
   const int64_t x0 = share.first(blockIdx.x);
@@ -631,32 +633,44 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
     tc_fence_after();
     tmem_dealloc(tmem, kDecTmemCols);
   }
+  // Nothing here needs the prefix's kernel, beside which this one may run; but this grid ends
+  // after it, so that the merge, which waits for this grid, has both.
+  if constexpr (!WHOLE) wait_dependencies();
 }
 
-// The units that the stream kernel cut, and the sequences without a key (zeros): one warp an
-// output row (b, head). The row's parts sit in the slots of CTAs c0 .. c1, those whose runs hold
-// tiles of the unit: slot 0 of each, or slot 1 of c0 when the unit is not the first of its run.
-// PREFIX: n_pre partials of the shared prefix ([n_pre][batch * Hq] rows before the rest of the
-// workspace) join, and a whole unit's partial is read from its own row.
-template <int D, int OUT, bool PREFIX>
+// The units that the stream kernel cut, and the sequences without a key (zeros): an output row
+// (b, head) at a time by WPR warps (1, or all 8 of a block, which take every 8th part: with 30 to
+// 40 parts a row one warp's loads came to 18 us, 64 blocks of them leaving the GPU idle). The
+// row's parts sit in the slots of CTAs c0 .. c1, those whose runs hold tiles of the unit: slot 0
+// of each, or slot 1 of c0 when the unit is not the first of its run. PREFIX: n_pre partials of
+// the shared prefix ([n_pre][batch * Hq] rows before the rest of the workspace) join, and a whole
+// unit's partial is read from its own row.
+constexpr int kMergeWarps = kStreamRuns / 32;
+
+template <int D, int OUT, bool PREFIX, int WPR>
 __global__ void __launch_bounds__(kStreamRuns) merge_stream_kernel(const PrefillArgs a0,
                                                                    int64_t grid_ctas,
                                                                    const float* pre_o,
                                                                    const float* pre_lse,
                                                                    int n_pre) {
-  __shared__ int64_t run[kStreamRuns + 1], wsum[kStreamRuns / 32];
+  static_assert(WPR == 1 || WPR == kMergeWarps, "a row takes a warp or the block");
+  constexpr int NV = D / 128;  // float4 columns a lane holds
+  __shared__ int64_t run[kStreamRuns + 1], wsum[kMergeWarps];
+  __shared__ float wpart[WPR > 1 ? kMergeWarps : 1][2];               // M and W of a warp's parts
+  __shared__ float4 opart[WPR > 1 ? kMergeWarps : 1][NV][32];         // their weighted rows
   stream_scan(a0, run, wsum, false);
   // Launched while the stream kernel ends (programmatic launch): its results are complete past
   // this wait. The lengths above were there before it.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_dependencies();
   const StreamShare share(run[kStreamRuns], grid_ctas);
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x / 32;
   const int64_t rows = (int64_t)a0.batch * a0.Hq;
   const int per = stream_per(a0);
   PrefillArgs a = a0;
-  constexpr int NV = D / 128;  // float4 columns a lane holds
-  for (int64_t row = (int64_t)blockIdx.x * (kStreamRuns / 32) + threadIdx.x / 32; row < rows;
-       row += (int64_t)gridDim.x * (kStreamRuns / 32)) {
+  const int first = WPR > 1 ? wid : 0;  // this warp's first part
+  constexpr int64_t kRows = kMergeWarps / WPR;  // rows of a block
+  for (int64_t row = (int64_t)blockIdx.x * kRows + wid / WPR; row < rows;
+       row += (int64_t)gridDim.x * kRows) {
     const int64_t b = div_pos(row, a.Hq), in_run = div_pos(b, per);
     const int head = (int)(row - b * a.Hq), g = head / a.G;
     bool bad;
@@ -690,15 +704,17 @@ __global__ void __launch_bounds__(kStreamRuns) merge_stream_kernel(const Prefill
       *o = a.ws_o + r * D;
       *lse = a.ws_lse + r;
     };
-    auto lse_of = [&](int64_t p) -> float {
+    // This warp's parts: first, first + WPR, ... (lane i holds the LSE of the i-th of 32).
+    const int64_t mine = total > first ? (total - first + WPR - 1) / WPR : 0;
+    auto lse_of = [&](int64_t i) -> float {
+      if (i >= mine) return -INFINITY;
       const float *o, *lse;
-      if (p >= total) return -INFINITY;
-      place(p, &o, &lse);
+      place(first + i * WPR, &o, &lse);
       return *lse;
     };
-    const float lse0 = lse_of(lane);  // part `lane`; more than 32 are read again below
+    const float lse0 = lse_of(lane);
     float M = lse0;
-    for (int64_t p = 32 + lane; p < total; p += 32) M = fmaxf(M, lse_of(p));
+    for (int64_t i = 32 + lane; i < mine; i += 32) M = fmaxf(M, lse_of(i));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float W = 0.f;
@@ -706,25 +722,25 @@ __global__ void __launch_bounds__(kStreamRuns) merge_stream_kernel(const Prefill
 #pragma unroll
     for (int v = 0; v < NV; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int kGroup = 8 / NV;  // parts loaded together
-    for (int64_t p32 = 0; M != -INFINITY && p32 < total; p32 += 32) {
-      const float lse = p32 == 0 ? lse0 : lse_of(p32 + lane);
+    for (int64_t i32 = 0; M != -INFINITY && i32 < mine; i32 += 32) {
+      const float lse = i32 == 0 ? lse0 : lse_of(i32 + lane);
       const float wl = lse == -INFINITY ? 0.f : exp2f(lse - M);
-      const int np32 = total - p32 < 32 ? (int)(total - p32) : 32;
-      for (int p0 = 0; p0 < np32; p0 += kGroup) {
+      const int n32 = mine - i32 < 32 ? (int)(mine - i32) : 32;
+      for (int i0 = 0; i0 < n32; i0 += kGroup) {
         float4 x[kGroup][NV];
 #pragma unroll
         for (int k = 0; k < kGroup; ++k) {
-          if (p0 + k >= np32) continue;
+          if (i0 + k >= n32) continue;
           const float *o, *l;
-          place(p32 + p0 + k, &o, &l);
+          place(first + (i32 + i0 + k) * WPR, &o, &l);
 #pragma unroll
           for (int v = 0; v < NV; ++v)
             x[k][v] = *reinterpret_cast<const float4*>(o + lane * 4 + 128 * v);
         }
 #pragma unroll
         for (int k = 0; k < kGroup; ++k) {
-          const float w = __shfl_sync(0xffffffffu, wl, (p0 + k) & 31);
-          if (p0 + k >= np32 || w == 0.f) continue;
+          const float w = __shfl_sync(0xffffffffu, wl, (i0 + k) & 31);
+          if (i0 + k >= n32 || w == 0.f) continue;
           W += w;
 #pragma unroll
           for (int v = 0; v < NV; ++v) {
@@ -736,11 +752,40 @@ __global__ void __launch_bounds__(kStreamRuns) merge_stream_kernel(const Prefill
         }
       }
     }
+    if constexpr (WPR > 1) {  // the warps' sums join (their weights brought to one maximum)
+      if (lane == 0) {
+        wpart[wid][0] = M;
+        wpart[wid][1] = W;
+      }
+#pragma unroll
+      for (int v = 0; v < NV; ++v) opart[wid][v][lane] = acc[v];
+      __syncthreads();
+      if (wid < NV) {  // warp v: the 128 columns from 128 v on
+        float Mt = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) Mt = fmaxf(Mt, wpart[w][0]);
+        W = 0.f;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) {
+          const float f = wpart[w][0] == -INFINITY ? 0.f : exp2f(wpart[w][0] - Mt);
+          const float4 x = opart[w][wid][lane];
+          W = fmaf(f, wpart[w][1], W);
+          sum.x = fmaf(f, x.x, sum.x);
+          sum.y = fmaf(f, x.y, sum.y);
+          sum.z = fmaf(f, x.z, sum.z);
+          sum.w = fmaf(f, x.w, sum.w);
+        }
+        acc[0] = sum;
+      }
+      __syncthreads();  // before the next row's sums
+      if (wid >= NV) continue;
+    }
     const float inv = W > 0.f ? 1.f / W : 0.f;
     uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + row * D;
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-      *reinterpret_cast<uint2*>(dst + lane * 4 + 128 * v) =
+    for (int v = 0; v < (WPR > 1 ? 1 : NV); ++v)
+      *reinterpret_cast<uint2*>(dst + lane * 4 + 128 * (WPR > 1 ? wid : v)) =
           make_uint2(pack2<OUT == kOutBf16>(acc[v].x * inv, acc[v].y * inv),
                      pack2<OUT == kOutBf16>(acc[v].z * inv, acc[v].w * inv));
   }

@@ -849,6 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  if constexpr (PRE) launch_dependents();  // the own part's kernel needs none of this one's work
   int64_t qt, kt0, kt1;
   int g, s, slot = kSlotUniform;
   if (a.balanced) {
@@ -1058,6 +1059,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kOutF32 = 0, kOutF16 = 1, kOutBf16 = 2;
 
 #include "prefill_pair.cuh"
+#include "prefill_duo.cuh"
 #include "decode_kernel.cuh"
 #include "decode_stream.cuh"
 #include "kv_append.cuh"
@@ -1331,6 +1333,25 @@ cudaError_t launch_pair(int64_t grid, cudaStream_t st, const CUtensorMap& tk,
   return cudaGetLastError();
 }
 
+template <int D, bool BF16>
+cudaError_t launch_duo(int64_t grid, cudaStream_t st, const CUtensorMap& tk, const CUtensorMap& tv,
+                       const PrefillArgs& a, const ItemTable& it) {
+  auto kern = prefill_duo_kernel<D, BF16>;
+  static std::atomic<uint64_t> configured{0};  // one bit per device ordinal
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(configured.load() & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             DuoCfg<D>::LAUNCH_SMEM);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit);
+  }
+  kern<<<(unsigned)grid, kDuoThreads, DuoCfg<D>::LAUNCH_SMEM, st>>>(tk, tv, a, it);
+  return cudaGetLastError();
+}
+
 template <int D>
 cudaError_t launch_d(bool paged, bool bf16, int64_t grid, cudaStream_t st, const CUtensorMap& tk,
                      const CUtensorMap& tv, const PrefillArgs& a, const ItemTable& it) {
@@ -1389,7 +1410,8 @@ cudaError_t launch_decode_d(int D, bool bf16, int64_t grid, cudaStream_t st,
 
 // The stream kernel on `ctas` CTAs, then its merge (programmatic launch: the merge's launch
 // overlaps the stream kernel's end). a.ws_o / ws_lse: the rows of the stream kernel's partials.
-// PREFIX: every unit leaves a partial, and n_pre partials of the prefix join (see the kernels).
+// PREFIX: every unit leaves a partial, and n_pre partials of the prefix join (see the kernels);
+// the stream kernel's launch overlaps the prefix's kernel before it.
 template <int D, bool BF16, bool PREFIX>
 cudaError_t launch_stream(int64_t ctas, cudaStream_t st, const CUtensorMap& tk,
                           const CUtensorMap& tv, const PrefillArgs& a, const float* pre_o,
@@ -1398,22 +1420,33 @@ cudaError_t launch_stream(int64_t ctas, cudaStream_t st, const CUtensorMap& tk,
   cudaError_t e = configure_decode(decode_stream_kernel<D, BF16, !PREFIX>,
                                    StreamCfg<D>::LAUNCH_SMEM, configured);
   if (e != cudaSuccess) return e;
-  decode_stream_kernel<D, BF16, !PREFIX>
-      <<<(unsigned)ctas, kThreads, StreamCfg<D>::LAUNCH_SMEM, st>>>(tk, tv, a);
-  e = cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t main = {};
+  main.gridDim = dim3((unsigned)ctas, 1, 1);
+  main.blockDim = dim3(kThreads, 1, 1);
+  main.dynamicSmemBytes = StreamCfg<D>::LAUNCH_SMEM;
+  main.stream = st;
+  main.attrs = attr;
+  main.numAttrs = PREFIX ? 1 : 0;
+  e = cudaLaunchKernelEx(&main, decode_stream_kernel<D, BF16, !PREFIX>, tk, tv, a);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = ceil_div64((int64_t)a.batch * a.Hq, kStreamRuns / 32);
+  // A block a row where a row has eight parts or more, and a warp a row where it has a few (most
+  // often none: the stream kernel wrote it).
+  const int64_t rows = (int64_t)a.batch * a.Hq;
+  const bool block_rows = n_pre + ctas / ((int64_t)a.batch * a.Hkv) >= 8;
+  const int64_t blocks = block_rows ? rows : ceil_div64(rows, kMergeWarps);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min<int64_t>(blocks, 4 * 148), 1, 1);
   cfg.blockDim = dim3(kStreamRuns, 1, 1);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_stream_kernel<D, BF16 ? kOutBf16 : kOutF16, PREFIX>, a,
-                            ctas, pre_o, pre_lse, n_pre);
+  constexpr int OUT = BF16 ? kOutBf16 : kOutF16;
+  auto kern = block_rows ? merge_stream_kernel<D, OUT, PREFIX, kMergeWarps>
+                         : merge_stream_kernel<D, OUT, PREFIX, 1>;
+  return cudaLaunchKernelEx(&cfg, kern, a, ctas, pre_o, pre_lse, n_pre);
 }
 
 template <bool PREFIX>
@@ -1857,7 +1890,8 @@ static int rebuild_batch(const pa_plan_t* plan, const Window* win, const int32_t
   const int D = plan->head_dim;
   if (D != 64 && D != 128 && D != 256) return PA_ERR_UNSUPPORTED;
   if (plan->n_kv_heads <= 0 || plan->n_q_heads != plan->n_kv_heads * plan->group ||
-      plan->ctas_per_unit != batch_ctas_per_unit(D, plan->group, plan->batch, q_lens))
+      plan->ctas_per_unit != (win ? window_q_tiles_per_unit(plan->group, plan->batch, q_lens)
+                                  : batch_ctas_per_unit(D, plan->group, plan->batch, q_lens)))
     return PA_ERR_INVALID_ARG;
   const int st = describe_batch(plan->batch, q_lens, hist_lens, plan->group, plan->n_kv_heads,
                                 plan->ctas_per_unit, bt);
@@ -1890,16 +1924,17 @@ static int run_batch(const pa_plan_t* plan, const Window* win, const Batch& bt,
   if (num_pages * PS + kTileKeys >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
   const bool bf16 = plan->dtype == PA_BF16;
   const int64_t rows = num_pages * PS;
-  const int k_rows = per == 2 ? std::min(PS, 64) : PS;
-  const int v_rows = per == 2 ? std::min(PS, 64) : std::min(PS, 128 / (D / 64));
-  const int v_panels = per == 2 ? 2 : D / 64;
-  const bool k_atoms = per == 2 && PS == 16;  // as in pa_prefill
+  const bool pair = per == 2 && D == 256;  // else two Q tiles a unit are one CTA's (windows)
+  const int k_rows = pair ? std::min(PS, 64) : PS;
+  const int v_rows = pair ? std::min(PS, 64) : std::min(PS, 128 / (D / 64));
+  const int v_panels = pair ? 2 : D / 64;
+  const bool k_atoms = pair && PS == 16;  // as in pa_prefill
   CUtensorMap tk, tv, tq;
   if (!(k_atoms ? make_v_map(&tk, k_pool, bf16, D, plan->n_kv_heads, rows, 8, D / 64)
                 : make_k_map(&tk, k_pool, bf16, D, plan->n_kv_heads, rows, k_rows)) ||
       !make_v_map(&tv, v_pool, bf16, D, plan->n_kv_heads, rows, v_rows, v_panels))
     return PA_ERR_CUDA;
-  const bool q_tma = per == 2 && kTileRows % plan->group == 0;
+  const bool q_tma = pair && kTileRows % plan->group == 0;
   if (q_tma && !make_q_map(&tq, q, bf16, D, plan->group, plan->n_kv_heads, (int)bt.total_rows))
     return PA_ERR_CUDA;
   if (!q_tma) memset(&tq, 0, sizeof tq);
@@ -1938,7 +1973,7 @@ static int run_batch(const pa_plan_t* plan, const Window* win, const Batch& bt,
   thread_local ItemTable table;
   for (size_t i = 0; i < sch.items.size(); ++i) table.item[i] = sch.items[i];
   for (size_t i = 0; i < bt.seq.size(); ++i) table.seq[i] = bt.seq[i];
-  const int64_t grid = plan->units * per;
+  const int64_t grid = plan->units * (pair ? 2 : 1);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   int max_rows = 0;  // small Q when no sequence's Q tile holds more than 8 packed rows
   for (const PaSeq& sq : bt.seq) max_rows = std::max(max_rows, (int)sq.rows);
@@ -1947,9 +1982,15 @@ static int run_batch(const pa_plan_t* plan, const Window* win, const Batch& bt,
       batch_decode_swapped(D, plan->group, per, bt.seq.data(), (int)bt.seq.size());
   cudaError_t e;
   if (win) {
-    if (per == 2)
+    if (pair)
       e = bf16 ? launch_pair<true, true, true>(grid, cs, tk, tv, tq, a, table)
                : launch_pair<true, false, true>(grid, cs, tk, tv, tq, a, table);
+    else if (per == 2 && D == 128)
+      e = bf16 ? launch_duo<128, true>(grid, cs, tk, tv, a, table)
+               : launch_duo<128, false>(grid, cs, tk, tv, a, table);
+    else if (per == 2)
+      e = bf16 ? launch_duo<64, true>(grid, cs, tk, tv, a, table)
+               : launch_duo<64, false>(grid, cs, tk, tv, a, table);
     else if (swapped)
       e = launch_decode_d<true, true>(D, bf16, grid, cs, tk, tv, a, table);
     else

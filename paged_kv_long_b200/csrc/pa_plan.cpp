@@ -345,6 +345,12 @@ int batch_ctas_per_unit(int head_dim, int G, int batch, const int32_t* q_lens) {
   return head_dim == 256 && max_qt > 1 ? 2 : 1;
 }
 
+int window_q_tiles_per_unit(int G, int batch, const int32_t* q_lens) {
+  int64_t max_qt = 0;
+  for (int b = 0; b < batch; ++b) max_qt = std::max(max_qt, q_tiles_for(q_lens[b], G));
+  return max_qt > 1 ? 2 : 1;
+}
+
 bool build_batch(int num_sms, int head_dim, int per, int G, int Hkv, const Batch& bt,
                  Schedule* out, const Window* win) {
   // One-row batches on the swapped decode kernel: two CTA slots per SM.
@@ -354,7 +360,8 @@ bool build_batch(int num_sms, int head_dim, int per, int G, int Hkv, const Batch
   if (!win && bt.seq.size() == 1 && per == ctas_per_unit_for(head_dim))
     return balanced_piece(q_tiles_for(bt.seq[0].rows, G), bt.seq[0].rows, bt.seq[0].hist, G,
                           Hkv, head_dim, num_sms, out);
-  const int slots = std::max(1, num_sms / per);
+  // a row block's worker: an SM, or an SM pair at head dim 256
+  const int slots = std::max(1, head_dim == 256 ? num_sms / per : num_sms);
   std::vector<int64_t> len;
   for (const PaSeq& sq : bt.seq) {
     const int64_t q_tiles = q_tiles_for(sq.rows, G);
@@ -415,7 +422,8 @@ static int plan_batch(int num_sms, int n_q_heads, int n_kv_heads, int head_dim, 
   for (int b = 0; b < batch; ++b)
     if (q_lens[b] < 0) return PA_ERR_INVALID_ARG;
   // CTA pairs only when some sequence has two Q tiles to pair; else one CTA per row block
-  const int per = pa::batch_ctas_per_unit(head_dim, G, batch, q_lens);
+  const int per = win ? pa::window_q_tiles_per_unit(G, batch, q_lens)
+                      : pa::batch_ctas_per_unit(head_dim, G, batch, q_lens);
   pa::Batch bt;
   const int st = pa::describe_batch(batch, q_lens, hist_lens, G, n_kv_heads, per, &bt);
   if (st != PA_OK) return st;

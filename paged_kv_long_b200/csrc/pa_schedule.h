@@ -35,6 +35,9 @@ int describe_batch(int batch, const int32_t* q_lens, const int64_t* hist_lens, i
 // CTAs per row block of a batch: 2 (CTA pairs, head dim 256) only when some sequence has two
 // or more Q tiles; a batch of one-tile sequences (decode) would leave half of every pair idle.
 int batch_ctas_per_unit(int head_dim, int G, int batch, const int32_t* q_lens);
+// Q tiles per row block of a windowed batch: 2 when some sequence has two or more (a CTA pair at
+// head dim 256, one CTA below), else 1.
+int window_q_tiles_per_unit(int G, int batch, const int32_t* q_lens);
 // The balanced schedule of a batch (row blocks of all sequences, longest first). With a window
 // (win non-null) a row block's tiles are those its rows' windows and the sinks reach, and its
 // items' [kt0, kt1) count along that list (window_tiles).

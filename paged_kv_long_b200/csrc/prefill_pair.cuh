@@ -283,6 +283,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();  // 0 issues the MMAs
 
+  if constexpr (PRE) launch_dependents();  // the own part's kernel needs none of this one's work
   int64_t tp, kt0, kt1;
   int g, s, slot = kSlotUniform;
   if (a.balanced) {

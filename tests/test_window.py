@@ -493,27 +493,30 @@ def test_gpu_window_fuzz(seed):
 
 @_gpu
 def test_gpu_repeated_runs_and_full_windows_agree_with_the_framework():
-    """Bit for bit the same on a second run; a window of the whole sequence equals pa_batch_prefill
-    and pa_decode rounded to the type (units in one piece each: the same arithmetic)."""
+    """Bit for bit the same on a second run. A window of the whole sequence is pa_batch_prefill and
+    pa_decode rounded to the type: both sides are within the bound of the 64-bit values (theirs
+    without the output's rounding), so they are within twice that of one another."""
     import torch
     bd = _binding()
-    c = Case(7, [33, 1], [100, 300], 10**6, 0, 8, 2, 128, 16, "f16")
-    _, a = run_prefill(c)
-    _, b = run_prefill(c)
-    assert torch.equal(a, b)
-    bp = bd.batch_plan(8, 2, 128, 16, c.rows, c.hist, "f16")
-    q, k, v, t = c.device()
-    want = bd.batch_prefill(bp, q, k, v, t)
-    if bp.plan.ws_bytes == 0:
-        assert torch.equal(a, want.half())
-    c = Case(8, [1, 1], [100, 300], 10**6, 0, 8, 2, 128, 16, "f16")
-    _, a = run_decode(c)
-    assert torch.equal(a, run_decode(c)[1])
-    q, k, v, t = c.device()
-    dp = bd.decode_plan(8, 2, 128, 16, 2, 301, "f16", splits=1)
-    want = bd.decode(dp, q, k, v, t, torch.tensor([101, 301], dtype=torch.int32, device="cuda"))
-    # the parts of cut units join in fp32: equal up to the one rounding
-    assert (a - want.half().cpu()).abs().max() <= 2 * torch.finfo(torch.float16).eps * a.abs().max()
+    for seed, D, Hq in ((7, 128, 8), (8, 256, 8), (9, 64, 4)):
+        c = Case(seed, [33, 1], [100, 300], 10**6, 0, Hq, 2, D, 16, "f16")
+        _, a = run_prefill(c)
+        _, b = run_prefill(c)
+        assert torch.equal(a, b)
+        q, k, v, t = c.device()
+        bp = bd.batch_plan(Hq, 2, D, 16, c.rows, c.hist, "f16")
+        want = bd.batch_prefill(bp, q, k, v, t)
+        _, _, lim = c.oracle()
+        assert (np.abs((a.double() - want.double()).cpu().numpy()) <= 2 * lim).all()
+        c = Case(seed + 10, [1, 1], [100, 300], 10**6, 0, Hq, 2, D, 16, "f16")
+        _, a = run_decode(c)
+        assert torch.equal(a, run_decode(c)[1])
+        q, k, v, t = c.device()
+        dp = bd.decode_plan(Hq, 2, D, 16, 2, 301, "f16")
+        lens = torch.tensor([101, 301], dtype=torch.int32, device="cuda")
+        want = bd.decode(dp, q, k, v, t, lens).cpu()
+        _, _, lim = c.oracle()
+        assert (np.abs((a.double() - want.double()).numpy()) <= 2 * lim).all()
 
 
 @_gpu
