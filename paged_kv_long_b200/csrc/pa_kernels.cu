@@ -742,12 +742,13 @@ __device__ __forceinline__ void empty_unit(const PrefillArgs& a, int64_t qt, int
   }
 }
 
-// The copy warps of the single-CTA kernels (warp w of kIssuers): fill the ring of NSLOT 16 KB
+// The copy warps of the single-CTA kernels (warp w of ISSUERS): fill the ring of NSLOT 16 KB
 // slots at `ring` in the order K0, K1, V0, K2, V1, ..., V_{n-1} (see Cfg) for the n KV tiles
-// kt0 .. kt0 + n - 1 of KV head g, fill number q by warp q % kIssuers. full[i] / empty[i] are the slots'
+// kt0 .. kt0 + n - 1 of KV head g, fill number q by warp q % ISSUERS. full[i] / empty[i] are the slots'
 // barriers (8 bytes apart). pre_row0 / pre_row1: lane i's page row of tiles 0 / 1 (read
 // before the set-up). Every copy has landed when this returns.
-template <int NP, int NSLOT, int PANEL_LOG, bool PAGED, bool WIN = false>
+template <int NP, int NSLOT, int PANEL_LOG, bool PAGED, bool WIN = false,
+          int ISSUERS = kIssuers>
 __device__ __forceinline__ void kv_copy_role(const PrefillArgs& a, const CUtensorMap* tm_k,
                                              const CUtensorMap* tm_v, int g, int64_t kt0, int n,
                                              int w, uint32_t ring, uint32_t bar_full, uint32_t bar_empty,
@@ -795,7 +796,7 @@ __device__ __forceinline__ void kv_copy_role(const PrefillArgs& a, const CUtenso
       const uint32_t item = j == 0 ? 0u : 2u * j - 1u;
       for (int k = 0; k < NP && ok; ++k) {
         const uint32_t q = item * NP + k;
-        if ((int)(q % kIssuers) != w) continue;
+        if ((int)(q % ISSUERS) != w) continue;
         if (!(ok = acquire(q))) break;
         const uint32_t slot = q % NSLOT;
         if (lane < ppt)
@@ -808,7 +809,7 @@ __device__ __forceinline__ void kv_copy_role(const PrefillArgs& a, const CUtenso
       const uint32_t item = v_item(j - 1, n);
       for (int k = 0; k < NP && ok; ++k) {
         const uint32_t q = item * NP + k;
-        if ((int)(q % kIssuers) != w) continue;
+        if ((int)(q % ISSUERS) != w) continue;
         if (!(ok = acquire(q))) break;
         const uint32_t slot = q % NSLOT;
         const int b = k * vbox_per_slot + lane;        // box index inside the V tile
@@ -830,7 +831,7 @@ __device__ __forceinline__ void kv_copy_role(const PrefillArgs& a, const CUtenso
   // abort) are skipped.
   const uint32_t all_fills = 2u * n * NP;
   for (uint32_t q = all_fills > (uint32_t)NSLOT ? all_fills - NSLOT : 0; q < issued_end; ++q)
-    if ((int)(q % kIssuers) == w)
+    if ((int)(q % ISSUERS) == w)
       drain_wait(full(q % NSLOT), (q / NSLOT) & 1, abort_flag, tmo);
   __syncwarp();
 }
@@ -1335,7 +1336,7 @@ cudaError_t launch_pair(int64_t grid, cudaStream_t st, const CUtensorMap& tk,
 
 template <int D, bool BF16>
 cudaError_t launch_duo(int64_t grid, cudaStream_t st, const CUtensorMap& tk, const CUtensorMap& tv,
-                       const PrefillArgs& a, const ItemTable& it) {
+                       const CUtensorMap& tq, const PrefillArgs& a, const ItemTable& it) {
   auto kern = prefill_duo_kernel<D, BF16>;
   static std::atomic<uint64_t> configured{0};  // one bit per device ordinal
   int dev = 0;
@@ -1348,7 +1349,7 @@ cudaError_t launch_duo(int64_t grid, cudaStream_t st, const CUtensorMap& tk, con
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
-  kern<<<(unsigned)grid, kDuoThreads, DuoCfg<D>::LAUNCH_SMEM, st>>>(tk, tv, a, it);
+  kern<<<(unsigned)grid, kDuoThreads, DuoCfg<D>::LAUNCH_SMEM, st>>>(tk, tv, tq, a, it);
   return cudaGetLastError();
 }
 
@@ -1934,7 +1935,7 @@ static int run_batch(const pa_plan_t* plan, const Window* win, const Batch& bt,
                 : make_k_map(&tk, k_pool, bf16, D, plan->n_kv_heads, rows, k_rows)) ||
       !make_v_map(&tv, v_pool, bf16, D, plan->n_kv_heads, rows, v_rows, v_panels))
     return PA_ERR_CUDA;
-  const bool q_tma = pair && kTileRows % plan->group == 0;
+  const bool q_tma = per == 2 && kTileRows % plan->group == 0;
   if (q_tma && !make_q_map(&tq, q, bf16, D, plan->group, plan->n_kv_heads, (int)bt.total_rows))
     return PA_ERR_CUDA;
   if (!q_tma) memset(&tq, 0, sizeof tq);
@@ -1986,11 +1987,11 @@ static int run_batch(const pa_plan_t* plan, const Window* win, const Batch& bt,
       e = bf16 ? launch_pair<true, true, true>(grid, cs, tk, tv, tq, a, table)
                : launch_pair<true, false, true>(grid, cs, tk, tv, tq, a, table);
     else if (per == 2 && D == 128)
-      e = bf16 ? launch_duo<128, true>(grid, cs, tk, tv, a, table)
-               : launch_duo<128, false>(grid, cs, tk, tv, a, table);
+      e = bf16 ? launch_duo<128, true>(grid, cs, tk, tv, tq, a, table)
+               : launch_duo<128, false>(grid, cs, tk, tv, tq, a, table);
     else if (per == 2)
-      e = bf16 ? launch_duo<64, true>(grid, cs, tk, tv, a, table)
-               : launch_duo<64, false>(grid, cs, tk, tv, a, table);
+      e = bf16 ? launch_duo<64, true>(grid, cs, tk, tv, tq, a, table)
+               : launch_duo<64, false>(grid, cs, tk, tv, tq, a, table);
     else if (swapped)
       e = launch_decode_d<true, true>(D, bf16, grid, cs, tk, tv, a, table);
     else

@@ -6,7 +6,8 @@
 // them, reads S or stores P the unit idles; measured 2,450 cycles a tile at head dim 128, the
 // tensor cores 40 % busy. Here two softmax groups (warps 0-3 and 4-7, a thread a row) run on two
 // tiles that share every K/V tile, so one's exponentials fill the other's gaps and the K/V copies
-// are halved. Warp 8 issues the MMAs, warps 9-11 the copies (kv_copy_role).
+// are halved. Warps 8 and 9 issue the MMAs of tile A and of tile B, warps 10 and 11 the copies
+// (kv_copy_role, and Q by tensor copy where G divides 128).
 //
 // Tensor memory (512 columns): O of both tiles (D each), S of both (128 each). P (16-bit pairs, 64
 // columns) goes over the lower half of its S: a thread works through its row in chunks of 32
@@ -14,14 +15,21 @@
 // taken in a first pass over S, the exponentials in a second, so a thread holds 64 scores at a
 // time and 384 threads fit (168 registers each).
 //
-// MMA order: PV_A(j), QK_A(j+1), PV_B(j), QK_B(j+1): while one group's softmax runs, the other
-// tile's two products do. The commit that announces S(j) covers every MMA issued before it, PV of
-// tile j - 1 among them, so a softmax that has S(j) may rescale O without another wait. V rows
-// that no row of the unit sees are zeroed by the MMA warp before PV reads them (it has waited for
-// every earlier fill of the ring itself).
+// Each issuing warp runs PV(j), QK(j+1) of its tile: while one group's softmax works, the other
+// tile's two products do. A thread that issues for both tiles loses ~950 cycles a tile to its
+// commits and waits (4,850 cycles a pair of tiles; see prefill_pair.cuh on issuing threads). P is
+// announced in two halves, so that the first 64 keys' PV overlaps the second half's exponentials.
+// The two groups take turns: left alone they fall into step whenever both wait for a K/V tile, and
+// then share the special-function unit and the tensor cores by turns of 3,000 and 2,000 cycles.
+// The commit that announces S(j) covers every MMA its thread issued before, PV(j - 1) among them,
+// so a softmax that has S(j) may rescale O without another wait. V rows that no row of the unit
+// sees are zeroed by the issuing warps before their PV (each has waited for every earlier fill of
+// the ring itself; the other's zeros are the same).
 
 constexpr int kDuoThreads = 384;
-constexpr int kDuoMmaWarp = 8;
+constexpr int kDuoMmaWarp = 8;   // and 9: one per tile
+constexpr int kDuoCopyWarp = 10;  // and 11
+constexpr int kDuoCopyWarps = 2;
 
 template <int D>
 struct DuoCfg {
@@ -31,7 +39,9 @@ struct DuoCfg {
   static constexpr int RING_OFF = 2 * NP * kPanel;
   static constexpr int BAR_OFF = RING_OFF + NSLOT * kPanel;
   static constexpr int B_FULL = 0, B_EMPTY = NSLOT, B_QFULL = 2 * NSLOT, B_SFULL = 2 * NSLOT + 1,
-                       B_PFULL = 2 * NSLOT + 3, B_DONE = 2 * NSLOT + 5, N_BARS = 2 * NSLOT + 6;
+                       B_PFULL = 2 * NSLOT + 3,  // [tile][half of the keys]
+                       B_TURN = 2 * NSLOT + 7,   // [tile]: its softmax may start the next tile
+                       B_DONE = 2 * NSLOT + 9, N_BARS = 2 * NSLOT + 10;
   static constexpr int MISC_OFF = BAR_OFF + 8 * N_BARS;
   static constexpr int SMEM = MISC_OFF + 16;
   static constexpr int LAUNCH_SMEM = SMEM + 1024;
@@ -42,7 +52,6 @@ struct DuoCfg {
   static_assert(NSLOT * kPanel >= 2 * kTileRows * (D * 4 + 16), "staging needs the ring");
 };
 
-// Visibility of the 128 keys of the tile at key0 to a row whose last key is `limit`, a bit a key.
 __device__ __forceinline__ uint32_t low_bits(int n) {  // bits below n, n clamped to 0 .. 32
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
 }
@@ -53,7 +62,8 @@ __device__ __forceinline__ int clamp_tile(int64_t x) {
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kDuoThreads, 1)
     prefill_duo_kernel(const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a_in,
+                       const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ CUtensorMap tm_q, const PrefillArgs a_in,
                        const __grid_constant__ ItemTable items) {
   PrefillArgs a = a_in;  // rebased on the item's sequence
   using C = DuoCfg<D>;
@@ -78,8 +88,8 @@ __global__ void __launch_bounds__(kDuoThreads, 1)
   }
 
   int32_t pre_row0 = a.oob_row, pre_row1 = a.oob_row;
-  if (warp > kDuoMmaWarp) {
-    const bool report = warp == kDuoMmaWarp + 1;
+  if (warp >= kDuoCopyWarp) {
+    const bool report = warp == kDuoCopyWarp;
     pre_row0 = tile_page_row<true, true>(a, kt0, n, 0, lane, report);
     pre_row1 = tile_page_row<true, true>(a, kt0, n, 1, lane, report);
   }
@@ -90,21 +100,23 @@ __global__ void __launch_bounds__(kDuoThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < NSLOT; ++i) {
       mbar_init(bar(C::B_FULL + i), 1);
-      mbar_init(bar(C::B_EMPTY + i), 1);
+      mbar_init(bar(C::B_EMPTY + i), 2);  // both tiles' products have read it
     }
-    mbar_init(bar(C::B_QFULL), 8);
+    mbar_init(bar(C::B_QFULL), a.q_tma ? 1 : 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(C::B_SFULL + i), 1);
-      mbar_init(bar(C::B_PFULL + i), 4);
+      mbar_init(bar(C::B_TURN + i), 4);
     }
-    mbar_init(bar(C::B_DONE), 1);
+    for (int i = 0; i < 4; ++i) mbar_init(bar(C::B_PFULL + i), 4);
+    mbar_init(bar(C::B_DONE), 2);
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
   }
-  if (warp == kDuoMmaWarp + 1 && lane == 0) {
+  if (warp == kDuoCopyWarp && lane == 0) {
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
+    if (a.q_tma) tma_prefetch_desc(&tm_q);
   }
   if (warp == kDuoMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -124,7 +136,7 @@ __global__ void __launch_bounds__(kDuoThreads, 1)
     const int64_t tok = grow / a.G;
     const bool valid = tok < a.R;
     const int head = g * a.G + (int)(grow % a.G);
-    {
+    if (!a.q_tma) {
       const uint4* src =
           reinterpret_cast<const uint4*>(a.q + (valid ? (tok * a.Hq + head) * (int64_t)D : 0));
 #pragma unroll
@@ -144,7 +156,8 @@ __global__ void __launch_bounds__(kDuoThreads, 1)
     if (low < 0) low = 0;
     const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_s = t_lane + C::S_COL + 128u * grp, t_o = t_lane + (uint32_t)(D * grp);
-    const uint32_t sfull = bar(C::B_SFULL + grp), pfull = bar(C::B_PFULL + grp);
+    const uint32_t sfull = bar(C::B_SFULL + grp), pfull = bar(C::B_PFULL + 2 * grp);
+    const uint32_t turn = bar(C::B_TURN + grp), other_turn = bar(C::B_TURN + (grp ^ 1));
     const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
@@ -158,7 +171,10 @@ __global__ void __launch_bounds__(kDuoThreads, 1)
 #pragma unroll
       for (int w = 0; w < 4; ++w)
         vis[w] = low_bits(hi - 32 * w) & (~low_bits(lo - 32 * w) | low_bits(snk - 32 * w));
-      if (!warp_wait(sfull, (uint32_t)j & 1u, abort_flag, tmo)) {
+      // Tile A goes first; B's tile j starts when A's is half done, A's j + 1 when B's j is.
+      if (!warp_wait(sfull, (uint32_t)j & 1u, abort_flag, tmo) ||
+          ((grp == 1 || j > 0) &&
+           !warp_wait(turn, (uint32_t)(grp == 1 ? j : j - 1) & 1u, abort_flag, tmo))) {
         ok = false;
         break;
       }
@@ -224,6 +240,15 @@ __global__ void __launch_bounds__(kDuoThreads, 1)
           pk[c >> 1] = pack2<BF16>(p.x, p.y);
         }
         tmem_st16u(t_s + 16u * k, pk);
+        if (k == 1) {  // the first 64 keys
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(pfull);
+            mbar_arrive(other_turn);
+          }
+        }
 #pragma unroll
         for (int c = 0; c < 32; ++c) cur[c] = nxt[c];
       }
@@ -231,7 +256,7 @@ __global__ void __launch_bounds__(kDuoThreads, 1)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(pfull);
+      if (lane == 0) mbar_arrive(pfull + 8u);
     }
     // Both tiles' last products: the rows below go through the ring's memory.
     if (ok) ok = warp_wait(bar(C::B_DONE), 0, abort_flag, tmo);
@@ -245,19 +270,35 @@ __global__ void __launch_bounds__(kDuoThreads, 1)
       x.stage_off = C::RING_OFF + (uint32_t)(grp * kTileRows * (D * 4 + 16));
       write_row<D, true, false, BF16>(a, x, r, valid, tok, head, m_run, l_run, t_o);
     }
-  } else if (warp > kDuoMmaWarp) {
-    // ============================================================ TMA issuers (three warps)
-    kv_copy_role<NP, NSLOT, C::PANEL_LOG, true, true>(
-        a, &tm_k, &tm_v, g, kt0, n, warp - kDuoMmaWarp - 1, sb + C::RING_OFF, bar(C::B_FULL),
+  } else if (warp >= kDuoCopyWarp) {
+    // ============================================================ TMA issuers (two warps)
+    if (a.q_tma && warp == kDuoCopyWarp && lane == 0) {
+      // both tiles' panels: 128 / G whole tokens each; tokens past the sequence are other rows
+      // (or zeros past the batch), whose scores are masked
+      mbar_arrive_expect_tx(bar(C::B_QFULL), 2u * NP * kPanel);
+      for (int t = 0; t < 2; ++t)
+        for (int p = 0; p < NP; ++p)
+          tma_load_4d(sb + C::Q_OFF + (t * NP + p) * kPanel, &tm_q, bar(C::B_QFULL), p * 64, 0, g,
+                      a.q_row0 + (int32_t)((2 * tp + t) * (kTileRows / a.G)));
+    }
+    __syncwarp();
+    kv_copy_role<NP, NSLOT, C::PANEL_LOG, true, true, kDuoCopyWarps>(
+        a, &tm_k, &tm_v, g, kt0, n, warp - kDuoCopyWarp, sb + C::RING_OFF, bar(C::B_FULL),
         bar(C::B_EMPTY), pre_row0, pre_row1, abort_flag, tmo);
+    if (a.q_tma && warp == kDuoCopyWarp && lane == 0)
+      drain_wait(bar(C::B_QFULL), 0, abort_flag, tmo);
+    __syncwarp();
   } else {
-    // ============================================================ MMA issuer (lane 0)
+    // ============================================================ MMA issuers (lane 0 each)
+    const int grp = warp - kDuoMmaWarp;
     constexpr uint32_t idesc_qk = umma_idesc_f16(128, kTileKeys, BF16, false);
     constexpr uint32_t idesc_pv = umma_idesc_f16(128, D, BF16, true);
     constexpr uint32_t kSlotDesc = kPanel >> 4;
-    const uint64_t q_desc = smem_desc_sw128(sb + C::Q_OFF, 16, 1024);
+    const uint64_t q_desc =
+        smem_desc_sw128(sb + C::Q_OFF, 16, 1024) + (uint32_t)(grp * NP) * kSlotDesc;
     const uint64_t k_desc = smem_desc_sw128(sb + C::RING_OFF, 16, 1024);
     const uint64_t v_desc = smem_desc_sw128(sb + C::RING_OFF, (uint32_t)a.v_rows * 128u, 1024);
+    const uint32_t t_s = tmem + C::S_COL + 128u * grp, t_o = tmem + (uint32_t)(D * grp);
     auto k_fill = [&](int j) -> uint32_t { return (j == 0 ? 0u : 2u * j - 1u) * NP; };
     auto wait_fills = [&](uint32_t q0) -> bool {
       bool w_ok = true;
@@ -273,71 +314,82 @@ __global__ void __launch_bounds__(kDuoThreads, 1)
 #pragma unroll
       for (int p = 0; p < NP; ++p) umma_commit(bar(C::B_EMPTY + (q0 + p) % NSLOT));
     };
-    // S of group grp, tile j, over its S buffer: P of tile j - 1 there was read by the PV issued
-    // before (tcgen05.mma executes in issue order).
-    auto qk = [&](int grp, int j) {
+    // S(j) over S(j - 1) and its P, which the PV issued before has read (tcgen05.mma executes in
+    // issue order). The slots' descriptors are worked out before the wait that the products hang
+    // on: an issuing lane's index arithmetic measured ~100 cycles an MMA.
+    uint64_t kd[NP], vd[kTileKeys / 16];
+    auto k_descs = [&](int j) {
+#pragma unroll
+      for (int p = 0; p < NP; ++p) kd[p] = k_desc + ((k_fill(j) + p) % NSLOT) * kSlotDesc;
+    };
+    auto qk = [&](int j) {
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
-        const uint64_t ad = q_desc + (grp * NP + p) * kSlotDesc;
-        const uint64_t bd = k_desc + ((k_fill(j) + p) % NSLOT) * kSlotDesc;
+        const uint64_t ad = q_desc + p * kSlotDesc;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma_ss(tmem + C::S_COL + 128u * grp, ad + 2 * kk, bd + 2 * kk, idesc_qk,
-                  (p | kk) != 0 ? 1u : 0u);
+          umma_ss(t_s, ad + 2 * kk, kd[p] + 2 * kk, idesc_qk, (p | kk) != 0 ? 1u : 0u);
       }
       umma_commit(bar(C::B_SFULL + grp));
-    };
-    auto pv = [&](int grp, int j) {
-      const uint32_t q0 = v_item(j, n) * NP;
-#pragma unroll
-      for (int ks = 0; ks < kTileKeys / 16; ++ks) {
-        const uint32_t off = v_offset<NP, C::PANEL_LOG>(16u * ks, 0, a.v_shift);
-        umma_ts(tmem + (uint32_t)(D * grp), tmem + C::S_COL + 128u * grp + 8u * ks,
-                v_desc + ((q0 + (off >> 14)) % NSLOT) * kSlotDesc + ((off & (kPanel - 1)) >> 4),
-                idesc_pv, (j > 0 || ks > 0) ? 1u : 0u);
-      }
+      release(k_fill(j));
     };
     bool ok = warp_wait(bar(C::B_QFULL), 0, abort_flag, tmo) && wait_fills(k_fill(0));
-    if (ok && lane == 0) {
-      qk(0, 0);
-      qk(1, 0);
-      release(k_fill(0));
-    }
+    k_descs(0);
+    if (ok && lane == 0) qk(0);
+    __syncwarp();
     for (int j = 0; j < n && ok; ++j) {
       const uint32_t v0 = v_item(j, n) * NP;
       if (!(ok = wait_fills(v0))) break;
       const int64_t key0 = kv_tile<true>(a, kt0 + j) * kTileKeys;
       if (tile_unseen<true>(a, key0)) {
-        for (int k = lane; k < kTileKeys; k += 32) {
-          if (!key_unseen<true>(a, key0 + k)) continue;
-#pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            const uint32_t off = v_offset<NP, C::PANEL_LOG>((uint32_t)k, p, a.v_shift);
-            const uint32_t ra = slot_addr((v0 + (off >> 14)) % NSLOT) + (off & (kPanel - 1));
-#pragma unroll
-            for (int c = 0; c < 8; ++c) st_shared_v4(ra + c * 16, 0u, 0u, 0u, 0u);
+        // Unseen rows of pages that were loaded (the others arrived as zeros): behind the sinks
+        // and before the window to their pages' ends, and behind the sequence.
+        auto zero_rows = [&](int64_t from, int64_t to) {  // keys [from, to) of this tile
+          const int r0 = clamp_tile(from - key0), r1 = clamp_tile(to - key0);
+          for (int i = lane; i < (r1 - r0) * 8 * NP; i += 32) {
+            const uint32_t k = r0 + i / (8 * NP), c = i % (8 * NP);
+            const uint32_t off = v_offset<NP, C::PANEL_LOG>(k, c >> 3, a.v_shift);
+            st_shared_v4(slot_addr((v0 + (off >> 14)) % NSLOT) + (off & (kPanel - 1)) +
+                             (c & 7) * 16,
+                         0u, 0u, 0u, 0u);
           }
+        };
+        const int64_t ps1 = a.page_rows - 1;
+        if (a.sinks < a.win_lo) {
+          const int64_t page_end = (a.sinks + ps1) & ~ps1, page0 = a.win_lo & ~ps1;
+          zero_rows(a.sinks, page_end < a.win_lo ? page_end : a.win_lo);
+          zero_rows(page0 > a.sinks ? page0 : a.sinks, a.win_lo);
         }
+        zero_rows(a.total_keys, (a.total_keys + ps1) & ~ps1);
         fence_proxy_async_smem();
         __syncwarp();
       }
-#pragma unroll 1
-      for (int grp = 0; grp < 2 && ok; ++grp) {
-        ok = warp_wait(bar(C::B_PFULL + grp), (uint32_t)j & 1u, abort_flag, tmo);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-          pv(grp, j);
-          if (grp == 1) release(v0);
+      {
+        const uint32_t s0 = v0 % NSLOT;
+#pragma unroll
+        for (int ks = 0; ks < kTileKeys / 16; ++ks) {
+          const uint32_t off = v_offset<NP, C::PANEL_LOG>(16u * ks, 0, a.v_shift);
+          uint32_t sl = s0 + (off >> 14);
+          if (sl >= (uint32_t)NSLOT) sl -= NSLOT;
+          vd[ks] = v_desc + sl * kSlotDesc + ((off & (kPanel - 1)) >> 4);
         }
-        if (j + 1 == n) continue;
-        if (grp == 0) ok = wait_fills(k_fill(j + 1));
-        if (ok && lane == 0) {
-          qk(grp, j + 1);
-          if (grp == 1) release(k_fill(j + 1));
-        }
-        __syncwarp();
+        if (j + 1 < n) k_descs(j + 1);
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == 1 && ok && j + 1 < n) ok = wait_fills(k_fill(j + 1));
+        if (ok)
+          ok = warp_wait(bar(C::B_PFULL + 2 * grp + h), (uint32_t)j & 1u, abort_flag, tmo);
+        tc_fence_after();
+        if (ok && lane == 0) {
+#pragma unroll
+          for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+            umma_ts(t_o, t_s + 8u * ks, vd[ks], idesc_pv, (j > 0 || ks > 0) ? 1u : 0u);
+        }
+      }
+      if (ok && j + 1 < n && lane == 0) qk(j + 1);
+      if (ok && lane == 0) release(v0);
+      __syncwarp();
     }
     // Every issued MMA must finish before tensor memory is freed.
     if (lane == 0) {
