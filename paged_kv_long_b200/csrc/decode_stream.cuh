@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
           for (int q = 0; q < NP && ok; ++q)
             ok = warp_wait(bar(C::B_FULL + (seq0 + q) % NSLOT), ((seq0 + q) / NSLOT) & 1,
                            abort_flag, tmo);
-          if (ok && !live) {
+          if (ok && v_row_unclean<true>(as, key0 + t)) {
 #pragma unroll
             for (int q = 0; q < NP; ++q) {
               const uint32_t off = v_offset<NP, C::PANEL_LOG>((uint32_t)t, q, a.v_shift);

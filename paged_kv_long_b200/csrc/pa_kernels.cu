@@ -120,6 +120,17 @@ __device__ __forceinline__ bool key_unseen(const PrefillArgs& a, int64_t key) {
     return key >= a.total_keys || (key < a.win_lo && key >= a.sinks);
   return key >= a.total_keys;
 }
+// Its V row is not known to be finite in shared memory: with a window the pages between the sinks
+// and win_lo, and behind the table, arrived as zeros.
+template <bool WIN>
+__device__ __forceinline__ bool v_row_unclean(const PrefillArgs& a, int64_t key) {
+  if constexpr (WIN) {
+    const int64_t page0 = key & ~(int64_t)(a.page_rows - 1);  // its page's first key
+    return key_unseen<true>(a, key) && page0 < a.total_keys &&
+           (page0 < a.sinks || page0 + a.page_rows > a.win_lo);
+  }
+  return key_unseen<WIN>(a, key);
+}
 // The KV tile at key0 holds such a key. Its page may hold any bits there, and P is 0 for it,
 // but 0 * NaN is NaN inside the MMA, so the softmax warps zero those V rows first.
 template <bool WIN>
@@ -592,7 +603,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Softmax
               break;
             }
           }
-          const bool zero_me = key_unseen<WIN>(a, key0 + r);
+          const bool zero_me = v_row_unclean<WIN>(a, key0 + r);
           if (!v_tail(j, zero_me ? r : -1)) {
             ok = false;
             break;

@@ -233,7 +233,7 @@ __device__ __forceinline__ void softmax_pair_role(const PrefillArgs& a, const So
     // The sequence's last tile, partly past its end (paged pools), or a tile with keys outside
     // every window: this CTA's half of those V rows is zeroed in shared memory before PV reads it.
     const bool tail = PAGED && tile_unseen<WIN>(a, key0);
-    if (tail && !v_tail(j, key_unseen<WIN>(a, key0 + r) ? r : -1)) {
+    if (tail && !v_tail(j, v_row_unclean<WIN>(a, key0 + r) ? r : -1)) {
       ok = false;
       break;
     }
