@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
 constexpr int kMergeWarps = kStreamRuns / 32;
 
 template <int D, int OUT, bool PREFIX, int WPR>
-__global__ void __launch_bounds__(kStreamRuns) merge_stream_kernel(const PrefillArgs a0,
+__global__ void __launch_bounds__(kStreamRuns, WPR > 1 ? 4 : 1) merge_stream_kernel(const PrefillArgs a0,
                                                                    int64_t grid_ctas,
                                                                    const float* pre_o,
                                                                    const float* pre_lse,

@@ -427,20 +427,38 @@ __device__ __forceinline__ void write_row(const PrefillArgs& a, const SoftmaxCtx
   if (valid && ws_row >= 0) a.ws_lse[ws_row] = l_run > 0.f ? m_run + log2f(l_run) : -INFINITY;
 }
 
-// The lower limit on a row's scores of the tile at key0, by select: keys below the row's window
-// (limit its last key) or this launch's first key that are no sinks.
-__device__ __forceinline__ void mask_window(const PrefillArgs& a, int64_t limit, int64_t key0,
-                                            float (&sv)[kTileKeys]) {
-  int64_t below = limit + 1 - a.window;
-  if (below < a.first_key) below = a.first_key;
-  below -= key0;
-  if (below <= 0) return;
-  const int end = below < kTileKeys ? (int)below : kTileKeys;
-  const int64_t snk = a.sinks - key0;
-  const int first = snk < 0 ? 0 : snk < kTileKeys ? (int)snk : kTileKeys;
+__device__ __forceinline__ uint32_t low_bits(int n) {  // bits below n, n clamped to 0 .. 32
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+__device__ __forceinline__ int clamp_tile(int64_t x) {
+  return x < 0 ? 0 : x > kTileKeys ? kTileKeys : (int)x;
+}
+// Visible keys of the tile at key0 to a row, a bit a key: [0, hi) without [snk, lo), for its last
+// key `limit` and the first one `low` of its window. False when the warp's rows see every key.
+__device__ __forceinline__ bool visible_bits(const PrefillArgs& a, int64_t limit, int64_t low,
+                                             int64_t key0, uint32_t (&vis)[4]) {
+  const bool some = limit < key0 + kTileKeys - 1 ||
+                    (low > key0 && a.sinks < low && a.sinks < key0 + kTileKeys);
+  if (!__any_sync(0xffffffffu, some)) return false;
+  const int hi = clamp_tile(limit + 1 - key0);
+  const int lo = clamp_tile(low - key0), snk = clamp_tile(a.sinks - key0);
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+    vis[w] = low_bits(hi - 32 * w) & (~low_bits(lo - 32 * w) | low_bits(snk - 32 * w));
+  return true;
+}
+// The first key of a row's window (or of this launch), given its last key.
+__device__ __forceinline__ int64_t row_low(const PrefillArgs& a, int64_t limit) {
+  const int64_t low = limit + 1 - a.window;
+  return low > a.first_key ? low : a.first_key;
+}
+// Masked scores become -inf by select, whatever bits they held. One test of a bit a score: two
+// comparisons against the limits took four times as long (1,700 of 2,100 cycles before the row's
+// maximum was known).
+__device__ __forceinline__ void mask_tile(const uint32_t (&vis)[4], float (&sv)[kTileKeys]) {
 #pragma unroll
   for (int c = 0; c < kTileKeys; ++c)
-    if (c >= first && c < end) sv[c] = -INFINITY;
+    sv[c] = (vis[c >> 5] >> (c & 31)) & 1u ? sv[c] : -INFINITY;
 }
 
 // The last key that the row of token tok sees. PRE: token tok is sequence tok's one query row,
@@ -521,14 +539,18 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, const Softmax
       tmem_wait_ld();
 
       // causal mask by select (masked scores become -inf, whatever bits they held)
-      const int64_t rel64 = limit - key0;
-      if (rel64 < kTileKeys - 1) {
-        const int rel = rel64 < -1 ? -1 : (int)rel64;
+      if constexpr (WIN) {
+        uint32_t vis[4];
+        if (visible_bits(a, limit, row_low(a, limit), key0, vis)) mask_tile(vis, sv);
+      } else {
+        const int64_t rel64 = limit - key0;
+        if (rel64 < kTileKeys - 1) {
+          const int rel = rel64 < -1 ? -1 : (int)rel64;
 #pragma unroll
-        for (int c = 0; c < kTileKeys; ++c)
-          if (c > rel) sv[c] = -INFINITY;
+          for (int c = 0; c < kTileKeys; ++c)
+            if (c > rel) sv[c] = -INFINITY;
+        }
       }
-      if constexpr (WIN) mask_window(a, limit, key0, sv);
       // row max: eight independent chains, then a tree
       float mx8[8];
 #pragma unroll

@@ -52,13 +52,6 @@ struct DuoCfg {
   static_assert(NSLOT * kPanel >= 2 * kTileRows * (D * 4 + 16), "staging needs the ring");
 };
 
-__device__ __forceinline__ uint32_t low_bits(int n) {  // bits below n, n clamped to 0 .. 32
-  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-}
-__device__ __forceinline__ int clamp_tile(int64_t x) {
-  return x < 0 ? 0 : x > kTileKeys ? kTileKeys : (int)x;
-}
-
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kDuoThreads, 1)
     prefill_duo_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -152,8 +145,7 @@ __global__ void __launch_bounds__(kDuoThreads, 1)
       if (lane == 0) mbar_arrive(bar(C::B_QFULL));
     }
     const int64_t limit = valid ? a.hist_len + tok : -1;  // last key this row may see
-    int64_t low = limit + 1 - a.window;                   // first one that is no sink
-    if (low < 0) low = 0;
+    const int64_t low = row_low(a, limit);
     const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_s = t_lane + C::S_COL + 128u * grp, t_o = t_lane + (uint32_t)(D * grp);
     const uint32_t sfull = bar(C::B_SFULL + grp), pfull = bar(C::B_PFULL + 2 * grp);
@@ -163,14 +155,8 @@ __global__ void __launch_bounds__(kDuoThreads, 1)
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const int64_t key0 = kv_tile<true>(a, kt0 + j) * kTileKeys;
-      // visible keys of the tile: [0, hi) without [snk, lo)
-      const int hi = clamp_tile(limit + 1 - key0);
-      const int lo = clamp_tile(low - key0), snk = clamp_tile(a.sinks - key0);
-      const bool masked = __any_sync(0xffffffffu, hi < kTileKeys || snk < lo);
       uint32_t vis[4];
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-        vis[w] = low_bits(hi - 32 * w) & (~low_bits(lo - 32 * w) | low_bits(snk - 32 * w));
+      const bool masked = visible_bits(a, limit, low, key0, vis);
       // Tile A goes first; B's tile j starts when A's is half done, A's j + 1 when B's j is.
       if (!warp_wait(sfull, (uint32_t)j & 1u, abort_flag, tmo) ||
           ((grp == 1 || j > 0) &&
@@ -179,7 +165,6 @@ __global__ void __launch_bounds__(kDuoThreads, 1)
         break;
       }
       tc_fence_after();
-      // masked scores become -inf by select, whatever bits they held
       auto mask = [&](float (&s)[32], uint32_t v) {
 #pragma unroll
         for (int c = 0; c < 32; ++c) s[c] = (v >> c) & 1u ? s[c] : -INFINITY;

@@ -169,14 +169,18 @@ __device__ __forceinline__ void softmax_pair_role(const PrefillArgs& a, const So
     }
 
     // causal mask by select (masked scores become -inf, whatever bits they held)
-    const int64_t rel64 = limit - key0;
-    if (rel64 < kTileKeys - 1) {
-      const int rel = rel64 < -1 ? -1 : (int)rel64;
+    if constexpr (WIN) {
+      uint32_t vis[4];
+      if (visible_bits(a, limit, row_low(a, limit), key0, vis)) mask_tile(vis, sv);
+    } else {
+      const int64_t rel64 = limit - key0;
+      if (rel64 < kTileKeys - 1) {
+        const int rel = rel64 < -1 ? -1 : (int)rel64;
 #pragma unroll
-      for (int c = 0; c < kTileKeys; ++c)
-        if (c > rel) sv[c] = -INFINITY;
+        for (int c = 0; c < kTileKeys; ++c)
+          if (c > rel) sv[c] = -INFINITY;
+      }
     }
-    if constexpr (WIN) mask_window(a, limit, key0, sv);
     // row max: eight independent chains, then a tree
     float mx8[8];
 #pragma unroll
