@@ -2220,12 +2220,12 @@ static int run_qk_rope(RopeArgs& a, bool interleaved, cudaStream_t st) {
   const int64_t n = std::max<int64_t>(1, a.rows * (q_sets + kv_sets) / (148 * 32));
   a.q_warps = (int)((q_sets + n - 1) / n);
   a.kv_warps = (int)((kv_sets + n - 1) / n);
-  const int64_t blocks = ((int64_t)a.rows * (a.q_warps + a.kv_warps) + 7) / 8;
-  if (blocks * 8 >= (int64_t(1) << 32)) return PA_ERR_UNSUPPORTED;
+  const int64_t blocks = (int64_t)a.rows * (a.q_warps + a.kv_warps);  // a warp each
+  if (blocks >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
   if (interleaved)
-    qk_rope_append_kernel<D, BF16, true><<<(unsigned)blocks, 256, 0, st>>>(a);
+    qk_rope_append_kernel<D, BF16, true><<<(unsigned)blocks, 32, 0, st>>>(a);
   else
-    qk_rope_append_kernel<D, BF16, false><<<(unsigned)blocks, 256, 0, st>>>(a);
+    qk_rope_append_kernel<D, BF16, false><<<(unsigned)blocks, 32, 0, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 }  // namespace pa
