@@ -183,3 +183,122 @@ class PrefillRoutes:
                             self.outs["staged"][i], self.ws, stream)
             binding.combine(p, self.ws, self.outs["staged"][i], stream)
             binding.kv_publish(ks, vs, kp, vp, self.table, h, r, stream)
+
+
+class ServingBatch:
+    """One attention layer's cache for a batch of requests, advanced step by step on the current
+    stream: pages, positions and slots of the step's rows (block_tables), head norms, rotation and
+    the cache write (qk_rope_append), then attention — over a sliding window with sinks, over a
+    prefix that all requests share (decode steps), or over every key.
+
+    ``step`` takes ragged chunks with host lengths, ``decode`` one token per request with every
+    length on the device, so that ``capture_decode`` can record it once as a CUDA graph and each
+    replay is the next token's step. A shared prefix is written first (``write_prefix``); every
+    request then begins after it. Pages are taken from the free list in order and not given back.
+    """
+
+    def __init__(self, n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, dtype: str,
+                 batch: int, max_len: int, rope, num_pages: int, window: int = 0, n_sinks: int = 0,
+                 prefix_len: int = 0, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, device="cuda"):
+        import torch
+        if window and prefix_len:
+            raise ValueError("a shared prefix is not windowed: give one of window, prefix_len")
+        if prefix_len % page_size:
+            raise ValueError("prefix_len must be a multiple of the page size")
+        self.shape = (n_q_heads, n_kv_heads, head_dim, page_size)
+        self.dtype, self.batch, self.device = dtype, batch, torch.device(device)
+        self.window, self.n_sinks, self.prefix_len = window, n_sinks, prefix_len
+        self.rope, self.q_weight, self.k_weight = rope, q_weight, k_weight
+        self.eps, self.interleaved = eps, interleaved
+        dt = torch.bfloat16 if dtype == "bf16" else torch.float16
+        i32 = dict(dtype=torch.int32, device=self.device)
+        pool = (num_pages, page_size, n_kv_heads, head_dim)
+        self.k_pool = torch.zeros(pool, dtype=dt, device=self.device)
+        self.v_pool = torch.zeros(pool, dtype=dt, device=self.device)
+        self.free_pages = torch.arange(num_pages, **i32)
+        shared = prefix_len // page_size
+        self.prefix_table = self.free_pages[:shared]
+        self.block_table = torch.full((batch, -(-max_len // page_size)), -1, **i32)
+        self.block_table[:, :shared] = self.prefix_table
+        self.pages_used = torch.full((1,), shared, **i32)
+        self.hist_lens = torch.full((batch,), prefix_len, **i32)
+        self.ones = torch.ones(batch, **i32)
+        self.hist = np.full(batch, prefix_len, dtype=np.int64)  # the host's copy
+        self.q_rot = None                                       # the last step's rotated queries
+        args = (*self.shape, batch)
+        if window:
+            self.plan = binding.window_decode_plan(*args, max_len, window, n_sinks, dtype)
+        elif prefix_len:
+            self.plan = binding.prefix_decode_plan(*args, prefix_len, max_len, dtype)
+        else:
+            self.plan = binding.decode_plan(*args, max_len, dtype)
+
+    def _cache(self, q, k, v, q_lens, rows: int):
+        """Tables of the step, then the rotated queries; keys and values go into the pools."""
+        t = binding.block_tables(q_lens, self.hist_lens, self.free_pages, self.pages_used,
+                                 self.block_table, rows, self.shape[3], self.k_pool.shape[0])
+        self.q_rot = binding.qk_rope_append(q, k, v, t.positions, t.slots, self.rope, self.k_pool,
+                                            self.v_pool, self.q_weight, self.k_weight, self.eps,
+                                            self.interleaved)
+        self.pages_used.copy_(t.pages_used)
+        self.hist_lens.copy_(t.seq_lens)
+        return t
+
+    def write_prefix(self, q, k, v):
+        """The shared prefix's rows (prefix_len of them) into its pages; returns their causal
+        attention [prefix_len, Hq, D] fp32."""
+        import torch
+        Hq, Hkv, D, PS = self.shape
+        n = self.prefix_len
+        at = torch.arange(n, dtype=torch.int32, device=self.device)
+        slots = self.prefix_table[(at // PS).long()] * PS + at % PS
+        q = binding.qk_rope_append(q, k, v, at, slots, self.rope, self.k_pool, self.v_pool,
+                                   self.q_weight, self.k_weight, self.eps, self.interleaved)
+        p = binding.plan(Hq, Hkv, D, PS, n, 0, self.dtype)
+        return binding.prefill_combine(p, q, self.k_pool, self.v_pool, self.prefix_table)
+
+    def step(self, q, k, v, q_lens):
+        """Chunks of q_lens[b] rows (host lengths), packed in order; returns their attention
+        [sum q_lens, Hq, D] (fp32 without a window)."""
+        import torch
+        q_lens = np.ascontiguousarray(q_lens, dtype=np.int32)
+        hist = self.hist.copy()
+        lens = torch.from_numpy(q_lens).to(self.device)
+        self._cache(q, k, v, lens, int(q_lens.sum()))
+        self.hist += q_lens
+        if self.window:
+            wp = binding.window_plan(*self.shape, q_lens, hist, self.window, self.n_sinks,
+                                     self.dtype)
+            return binding.window_prefill(wp, self.q_rot, self.k_pool, self.v_pool,
+                                          self.block_table)
+        bp = binding.batch_plan(*self.shape, q_lens, hist, self.dtype)
+        return binding.batch_prefill(bp, self.q_rot, self.k_pool, self.v_pool, self.block_table)
+
+    def decode(self, q, k, v):
+        """One token per request; returns its attention [batch, Hq, D] (fp32 without a window or
+        a shared prefix). The host's lengths advance when this runs, not when a graph replays."""
+        t = self._cache(q, k, v, self.ones, self.batch)
+        self.hist += 1
+        pools = (self.k_pool, self.v_pool)
+        if self.window:
+            return binding.window_decode(self.plan, self.q_rot, *pools, self.block_table,
+                                         t.seq_lens)
+        if self.prefix_len:
+            return binding.prefix_decode(self.plan, self.q_rot, *pools, self.prefix_table,
+                                         self.block_table, t.seq_lens)
+        return binding.decode(self.plan, self.q_rot, *pools, self.block_table, t.seq_lens)
+
+    def capture_decode(self, q, k, v):
+        """The decode step on these (static) tensors as a CUDA graph: (graph, its output). Run
+        ``decode`` once before. Each replay is the next token's step: rewrite q, k and v in place,
+        replay, and count it with ``replayed`` before host lengths are needed again."""
+        import torch
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = self.decode(q, k, v)
+        self.hist -= 1  # captured, not run
+        return graph, out
+
+    def replayed(self, steps: int = 1):
+        self.hist += steps
