@@ -161,14 +161,27 @@ struct ItemTable {
   PaItem item[kMaxItems];
   PaSeq seq[kMaxSeqs];  // batched plans: the sequences, rb0 ascending
 };
+// The shared-prefix kernels run uniform splits only: a parameter of 12 KB less at each launch.
+struct NoTable {
+  PaItem item[1];
+  PaSeq seq[1];
+};
+template <bool PRE>
+struct TableOf {
+  using type = ItemTable;
+};
+template <>
+struct TableOf<true> {
+  using type = NoTable;
+};
 // SoftmaxCtx::slot value of the uniform-split schedule (destination from the split index).
 constexpr int kSlotUniform = -2;
 
 // Batched plans: point the arguments at the sequence that owns global row block rb (its Q and
 // output rows, its page-table row, its history and rows) and return the row block's number
 // within the sequence.
-template <int D, bool WIN = false>
-__device__ __forceinline__ int32_t batch_rebase(PrefillArgs& a, const ItemTable& t, int32_t rb) {
+template <int D, bool WIN = false, class Table>
+__device__ __forceinline__ int32_t batch_rebase(PrefillArgs& a, const Table& t, int32_t rb) {
   const int b = seq_of_rb(t.seq, a.batch, rb);
   const PaSeq sq = t.seq[b];
   a.q += (int64_t)sq.q_row0 * a.Hq * D;
@@ -873,7 +886,8 @@ __device__ __forceinline__ void kv_copy_role(const PrefillArgs& a, const CUtenso
 template <int D, bool PAGED, bool BF16, bool SQ, bool WIN, bool PRE>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                   const PrefillArgs a_in, const __grid_constant__ ItemTable items) {
+                   const PrefillArgs a_in,
+                   const __grid_constant__ typename TableOf<PRE>::type items) {
   PrefillArgs a = a_in;  // rebased on one sequence in batched plans and decode
   using C = Cfg<D, SQ>;
   constexpr int NP = C::NP, NSLOT = C::NSLOT;
@@ -886,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (PRE) launch_dependents();  // the own part's kernel needs none of this one's work
   int64_t qt, kt0, kt1;
   int g, s, slot = kSlotUniform;
-  if (a.balanced) {
+  if (!PRE && a.balanced) {
     const PaItem it = items.item[blockIdx.x];
     const int32_t rb = a.batch > 0 ? batch_rebase<D, WIN>(a, items, it.rb) : it.rb;
     rb_coords(rb, a.q_tiles, a.Hkv, &qt, &g);
@@ -1317,7 +1331,8 @@ bool make_q_map(CUtensorMap* map, const void* base, bool bf16, int D, int G, int
 
 template <int D, bool PAGED, bool BF16, bool SQ = false, bool WIN = false, bool PRE = false>
 cudaError_t launch_prefill(int64_t grid, cudaStream_t st, const CUtensorMap& tk,
-                           const CUtensorMap& tv, const PrefillArgs& a, const ItemTable& it) {
+                           const CUtensorMap& tv, const PrefillArgs& a,
+                           const typename TableOf<PRE>::type& it) {
   auto kern = prefill_kernel<D, PAGED, BF16, SQ, WIN, PRE>;
   static std::atomic<uint64_t> configured{0};  // one bit per device ordinal
   int dev = 0;
@@ -1337,7 +1352,7 @@ cudaError_t launch_prefill(int64_t grid, cudaStream_t st, const CUtensorMap& tk,
 template <bool PAGED, bool BF16, bool WIN = false, bool PRE = false>
 cudaError_t launch_pair(int64_t grid, cudaStream_t st, const CUtensorMap& tk,
                         const CUtensorMap& tv, const CUtensorMap& tq, const PrefillArgs& a,
-                        const ItemTable& it) {
+                        const typename TableOf<PRE>::type& it) {
   auto kern = prefill_pair_kernel<PAGED, BF16, WIN, PRE>;
   static std::atomic<uint64_t> configured{0};
   int dev = 0;
@@ -1839,20 +1854,20 @@ extern "C" int pa_prefix_decode(const pa_plan_t* plan, int64_t prefix_len, const
   const int64_t grid =
       ceil_div64(w.q_tiles, w.per) * plan->n_kv_heads * (int64_t)w.splits * w.per;
   if (grid >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
-  thread_local ItemTable table;  // unused
+  const NoTable none{};
   cudaError_t e;
   if (w.per == 2)
-    e = bf16 ? launch_pair<true, true, false, true>(grid, cs, pk, pv, pq, p, table)
-             : launch_pair<true, false, false, true>(grid, cs, pk, pv, pq, p, table);
+    e = bf16 ? launch_pair<true, true, false, true>(grid, cs, pk, pv, pq, p, none)
+             : launch_pair<true, false, false, true>(grid, cs, pk, pv, pq, p, none);
   else if (D == 64)
-    e = bf16 ? launch_prefill<64, true, true, false, false, true>(grid, cs, pk, pv, p, table)
-             : launch_prefill<64, true, false, false, false, true>(grid, cs, pk, pv, p, table);
+    e = bf16 ? launch_prefill<64, true, true, false, false, true>(grid, cs, pk, pv, p, none)
+             : launch_prefill<64, true, false, false, false, true>(grid, cs, pk, pv, p, none);
   else if (D == 128)
-    e = bf16 ? launch_prefill<128, true, true, false, false, true>(grid, cs, pk, pv, p, table)
-             : launch_prefill<128, true, false, false, false, true>(grid, cs, pk, pv, p, table);
+    e = bf16 ? launch_prefill<128, true, true, false, false, true>(grid, cs, pk, pv, p, none)
+             : launch_prefill<128, true, false, false, false, true>(grid, cs, pk, pv, p, none);
   else
-    e = bf16 ? launch_prefill<256, true, true, false, false, true>(grid, cs, pk, pv, p, table)
-             : launch_prefill<256, true, false, false, false, true>(grid, cs, pk, pv, p, table);
+    e = bf16 ? launch_prefill<256, true, true, false, false, true>(grid, cs, pk, pv, p, none)
+             : launch_prefill<256, true, false, false, false, true>(grid, cs, pk, pv, p, none);
   if (e != cudaSuccess) return PA_ERR_CUDA;
 
   // Every sequence's own keys, from the prefix's end on, and the merge of all partials.
@@ -1866,6 +1881,7 @@ extern "C" int pa_prefix_decode(const pa_plan_t* plan, int64_t prefix_len, const
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
   }
   a.splits = w.own.splits;
+  thread_local ItemTable table;  // unused by decode units
   e = launch_paged_single<true>(D, bf16, G <= 8, w.own.units, cs, tk, tv, a, table);
   if (e != cudaSuccess) return PA_ERR_CUDA;
   return merge_rows16(lse_ws, lse, out, w.splits + w.own.splits, rows, D, bf16, cs);

@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     prefill_pair_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_q, const PrefillArgs a_in,
-                        const __grid_constant__ ItemTable items) {
+                        const __grid_constant__ typename TableOf<PRE>::type items) {
   PrefillArgs a = a_in;  // rebased on one sequence in batched plans
   using C = PairCfg;
   constexpr int D = 256, NSLOT = C::NSLOT;
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   if constexpr (PRE) launch_dependents();  // the own part's kernel needs none of this one's work
   int64_t tp, kt0, kt1;
   int g, s, slot = kSlotUniform;
-  if (a.balanced) {
+  if (!PRE && a.balanced) {
     const PaItem it = items.item[blockIdx.x >> 1];
     const int32_t rb = a.batch > 0 ? batch_rebase<D, WIN>(a, items, it.rb) : it.rb;
     rb_coords(rb, (a.q_tiles + 1) / 2, a.Hkv, &tp, &g);
