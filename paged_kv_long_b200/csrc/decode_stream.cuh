@@ -34,49 +34,80 @@ struct StreamCfg {
                        B_MMADONE = 2 * NSLOT + 8, N_BARS = 2 * NSLOT + 9;
   static constexpr int RED_OFF = BAR_OFF + 8 * (N_BARS + 1);  // [2][4 warps][8 heads]
   static constexpr int SUM_OFF = RED_OFF + 2 * 4 * 8 * 4;     // [4 warps][8 heads]
-  static constexpr int RUN_OFF = SUM_OFF + 4 * 8 * 4;         // [kStreamRuns + 1] int64
-  static constexpr int MISC_OFF = RUN_OFF + 8 * (kStreamRuns + 1);
+  static constexpr int RUN_OFF = SUM_OFF + 4 * 8 * 4;         // [kStreamRuns + 1] slots
+  static constexpr int MISC_OFF = RUN_OFF + 4 * (kStreamRuns + 1);
   static constexpr int SMEM = MISC_OFF + 16;
   static constexpr int LAUNCH_SMEM = SMEM + 1024;
   static constexpr int PANEL_LOG = (NP == 4) ? 9 : 8;
-  static_assert(BAR_OFF % 8 == 0 && RUN_OFF % 8 == 0, "alignment");
+  static_assert(BAR_OFF % 8 == 0 && RED_OFF % 16 == 0 && MISC_OFF % 4 == 0, "alignment");
   static_assert(kDecCtasPerSm * (LAUNCH_SMEM + 1024) <= 233472, "two CTAs per SM");
 };
 
-// Slots of a unit of n tiles (none without tiles), and sequences of a run of the scan.
-__device__ __forceinline__ int64_t stream_slots(int64_t n) { return n > 0 ? n + 1 : 0; }
-__device__ __forceinline__ int stream_per(const PrefillArgs& a) {
-  return (int)(((int64_t)a.batch + kStreamRuns - 1) / kStreamRuns);
+// Keys, tiles and slots fit 32 bits here (the host sees to it: seq_cap, and the most slots below
+// 2^31): a CTA's start is a few hundred instructions that no cache holds yet, and 64-bit
+// arithmetic doubles them.
+
+// One sequence's keys and its tile list: tile v of the list is KV tile v for v < head, else
+// v + gap; the row sees key k < keys when k >= lo or k < sinks.
+struct StreamSeq {
+  int32_t keys, lo, head, gap;
+};
+__device__ __forceinline__ int32_t stream_tile(const StreamSeq& q, int32_t v) {
+  return v < q.head ? v : v + q.gap;
 }
-// x / y for x >= 0, y > 0, in 32 bits where both fit (a 64-bit division is ~600 cycles).
-__device__ __forceinline__ int64_t div_pos(int64_t x, int64_t y) {
-  if (((x | y) >> 32) == 0) return (int64_t)((uint32_t)x / (uint32_t)y);
-  return x / y;
+__device__ __forceinline__ bool stream_unseen(const StreamSeq& q, int32_t sinks, int32_t key) {
+  return key >= q.keys || (key < q.lo && key >= sinks);
+}
+
+// Sequence b's view (its length clamped into the table row; *bad: it was outside) and the number
+// of its tiles: none when it ends before first_key.
+__device__ __forceinline__ int32_t stream_seq(const PrefillArgs& a, int32_t b, StreamSeq& q,
+                                              bool* bad) {
+  int32_t len = __ldg(a.seq_lens + b);
+  if ((uint32_t)len > (uint32_t)a.seq_cap) {
+    *bad = true;
+    len = len < 0 ? 0 : a.seq_cap;
+  }
+  q.keys = len;
+  if (len <= a.first_key32) return 0;
+  q.lo = max(max(len - a.window32, 0), a.first_key32);
+  const int32_t w0 = q.lo / kTileKeys;
+  q.head = (int32_t)(((uint32_t)min(a.sinks32, len) + kTileKeys - 1) / kTileKeys);
+  q.gap = max(w0 - q.head, 0);
+  return (len - 1) / kTileKeys + 1 - q.gap;
+}
+
+// Slots of a unit of n tiles (none without tiles), and sequences of a run of the scan.
+__device__ __forceinline__ int32_t stream_slots(int32_t n) { return n > 0 ? n + 1 : 0; }
+__device__ __forceinline__ int32_t stream_per(const PrefillArgs& a) {
+  return (int32_t)(((uint32_t)a.batch + kStreamRuns - 1) / kStreamRuns);
 }
 
 // Slots before every run of sequences (run i: sequences [i per, (i + 1) per)), in all heads, into
 // run[0 .. kStreamRuns]; `wsum`: a word per warp. Every thread of the block (kStreamRuns of
 // them). Reports bad lengths when `report`.
-__device__ __forceinline__ void stream_scan(const PrefillArgs& a_in, int64_t* run, int64_t* wsum,
+__device__ __forceinline__ void stream_scan(const PrefillArgs& a, int32_t* run, int32_t* wsum,
                                             bool report) {
-  PrefillArgs a = a_in;
   const int t = threadIdx.x, lane = t & 31, wid = t >> 5;
-  const int per = stream_per(a);
-  const int64_t b0 = (int64_t)t * per, b1 = b0 + per < a.batch ? b0 + per : a.batch;
+  const int32_t per = stream_per(a);
   bool bad = false;
-  int64_t sum = 0;
-  for (int64_t b = b0; b < b1; ++b)
-    sum += stream_slots(stream_seq(a, b, &bad)) * a.Hkv;
+  int32_t sum = 0;
+  StreamSeq q;
+  for (int32_t i = 0; i < per; ++i) {
+    const int64_t b = (int64_t)t * per + i;
+    if (b < a.batch) sum += stream_slots(stream_seq(a, (int32_t)b, q, &bad));
+  }
+  sum *= a.Hkv;
   if (bad && report) atomicOr(&g_pa_error_flags, kFlagPage);
-  int64_t incl = sum;
+  int32_t incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    const int32_t v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
   if (lane == 31) wsum[wid] = incl;
   __syncthreads();
-  int64_t before = 0;
+  int32_t before = 0;
   for (int w = 0; w < wid; ++w) before += wsum[w];
   run[t + 1] = before + incl;
   if (t == 0) run[0] = 0;
@@ -87,59 +118,60 @@ __device__ __forceinline__ void stream_scan(const PrefillArgs& a_in, int64_t* ru
 // saves; one sequence at window 4,096 measured 16.5 us at two, 18.6 us at one) of q slots, the
 // first r of them q + 1.
 struct StreamShare {
-  int64_t C, q, r;
-  __device__ __forceinline__ StreamShare(int64_t T, int64_t ctas) {
-    C = T / 2 < ctas ? T / 2 : ctas;
-    q = C > 0 ? div_pos(T, C) : 0;
-    r = T - q * C;
+  uint32_t C, q, r;
+  __device__ __forceinline__ StreamShare(int32_t T, int64_t ctas) {
+    const uint32_t most = (uint32_t)ctas;
+    C = (uint32_t)T / 2 < most ? (uint32_t)T / 2 : most;
+    q = C > 0 ? (uint32_t)T / C : 0;
+    r = (uint32_t)T - q * C;
   }
-  __device__ __forceinline__ int64_t first(int64_t c) const { return c * q + (c < r ? c : r); }
-  __device__ __forceinline__ int64_t owner(int64_t x) const {
-    const int64_t big = r * (q + 1);
-    return x < big ? div_pos(x, q + 1) : r + div_pos(x - big, q);
+  __device__ __forceinline__ int32_t first(uint32_t c) const {
+    return (int32_t)(c * q + (c < r ? c : r));
+  }
+  __device__ __forceinline__ int32_t owner(int32_t x) const {
+    const uint32_t big = r * (q + 1), y = (uint32_t)x;
+    return (int32_t)(y < big ? y / (q + 1) : r + (y - big) / q);
   }
 };
 
 // A CTA's walk along its segments.
 struct StreamWalk {
-  int64_t b;        // sequence
-  int g;            // KV head
-  int64_t n_b;      // tiles of the unit
-  int64_t t0;       // first tile of the segment in the unit
-  int64_t left;     // slots of the CTA's run behind this segment
-  int n;            // tiles of the segment
-  int index;        // segments before this one
+  StreamSeq q;      // the sequence
+  int32_t b, g;     // which, and the KV head
+  int32_t n_b;      // tiles of the unit
+  int32_t t0;       // first tile of the segment in the unit
+  int32_t left;     // slots of the CTA's run behind this segment
+  int32_t n;        // tiles of the segment
+  int32_t index;    // segments before this one
 };
 
-// The segment at slot x of the whole list (a: pointed at its sequence) of a run of `slots`.
-__device__ __forceinline__ StreamWalk stream_start(PrefillArgs& a, const int64_t* run, int64_t x,
-                                                   int64_t slots) {
+// The segment at slot x of the whole list, of a run of `slots`.
+__device__ __forceinline__ StreamWalk stream_start(const PrefillArgs& a, const int32_t* run,
+                                                   int32_t x, int32_t slots) {
   StreamWalk s;
-  int lo = 0, hi = kStreamRuns - 1;
-  while (lo < hi) {  // the last run that begins at or before x
-    const int mid = (lo + hi + 1) >> 1;
-    if (run[mid] <= x) lo = mid;
-    else hi = mid - 1;
-  }
+  int lo = 0;
+#pragma unroll 1
+  for (int step = kStreamRuns / 2; step > 0; step >>= 1)  // the last run that begins at or before x
+    if (run[lo + step] <= x) lo += step;
   bool bad;
-  s.b = (int64_t)lo * stream_per(a);
-  int64_t off = x - run[lo];
+  s.b = lo * stream_per(a);
+  int32_t off = x - run[lo];
   for (;; ++s.b) {
-    s.n_b = stream_seq(a, s.b, &bad);
-    const int64_t all = stream_slots(s.n_b) * a.Hkv;
+    s.n_b = stream_seq(a, s.b, s.q, &bad);
+    const int32_t all = stream_slots(s.n_b) * a.Hkv;
     if (off < all || s.b + 1 >= a.batch) break;
     off -= all;
   }
-  s.g = (int)div_pos(off, s.n_b + 1);
+  s.g = (int32_t)((uint32_t)off / (uint32_t)(s.n_b + 1));
   off -= s.g * (s.n_b + 1);
-  const int64_t mine = s.n_b + 1 - off < slots ? s.n_b + 1 - off : slots;
+  const int32_t mine = min(s.n_b + 1 - off, slots);
   s.left = slots - mine;
   s.t0 = off > 0 ? off - 1 : 0;
-  s.n = (int)(off > 0 ? mine : mine - 1);  // >= 1: a run has two slots at least
+  s.n = off > 0 ? mine : mine - 1;  // >= 1: a run has two slots at least
   s.index = 0;
   return s;
 }
-__device__ __forceinline__ bool stream_next(PrefillArgs& a, StreamWalk& s) {
+__device__ __forceinline__ bool stream_next(const PrefillArgs& a, StreamWalk& s) {
   if (s.left <= 1) return false;  // one slot: the start of a unit that the next CTA has
   s.t0 = 0;
   ++s.index;
@@ -148,29 +180,23 @@ __device__ __forceinline__ bool stream_next(PrefillArgs& a, StreamWalk& s) {
     bool bad;
     do {
       if (s.b + 1 >= a.batch) return false;
-      s.n_b = stream_seq(a, ++s.b, &bad);
+      s.n_b = stream_seq(a, ++s.b, s.q, &bad);
     } while (s.n_b == 0);
   }
-  const int64_t mine = s.n_b + 1 < s.left ? s.n_b + 1 : s.left;
+  const int32_t mine = min(s.n_b + 1, s.left);
   s.left -= mine;
-  s.n = (int)(mine - 1);
+  s.n = mine - 1;
   return true;
-}
-// Point a's table row and its length at the walk's sequence.
-__device__ __forceinline__ void stream_table(PrefillArgs& a, const PrefillArgs& a0, int64_t b) {
-  a.page_table = a0.page_table + b * a.table_stride;
-  a.table_len = (a.total_keys + a.page_rows - 1) / a.page_rows;
 }
 
 // Copy warp w of kIssuers: the K/V tiles of all segments through the ring, as kv_copy_role does
 // for one unit (K0, K1, V0, K2, V1, ..., V_{n-1} within a segment, fill numbers running on).
 template <int NP, int NSLOT, int PANEL_LOG>
-__device__ __forceinline__ void stream_copy_role(const PrefillArgs& a0, const CUtensorMap* tm_k,
-                                                 const CUtensorMap* tm_v, const int64_t* run,
-                                                 int64_t x0, int64_t slots, int w, uint32_t ring,
+__device__ __forceinline__ void stream_copy_role(const PrefillArgs& a, const CUtensorMap* tm_k,
+                                                 const CUtensorMap* tm_v, const int32_t* run,
+                                                 int32_t x0, int32_t slots, int w, uint32_t ring,
                                                  uint32_t bar_full, uint32_t bar_empty,
                                                  volatile int* abort_flag, uint64_t tmo) {
-  PrefillArgs a = a0, an = a0;  // at the segment's sequence, and at the next one's
   const int lane = threadIdx.x & 31;
   auto slot_addr = [&](uint32_t slot) -> uint32_t { return ring + slot * kPanel; };
   auto full = [&](uint32_t slot) -> uint32_t { return bar_full + 8u * slot; };
@@ -179,6 +205,21 @@ __device__ __forceinline__ void stream_copy_role(const PrefillArgs& a0, const CU
   const int vbytes_log = a.v_shift + PANEL_LOG;   // log2 of a V box's bytes
   const int vbox_per_slot = 1 << (14 - vbytes_log);
   bool ok = true;
+  // Key-row coordinate in the pool of page `lane` of the segment's tile jt (tile_page_row): pages
+  // that the row does not see arrive as zeros.
+  auto fetch = [&](const StreamWalk& seg, int jt) -> int32_t {
+    int32_t row = a.oob_row;
+    const int32_t lp = stream_tile(seg.q, seg.t0 + jt) * ppt + lane, page0 = lp << a.page_shift;
+    if (jt < seg.n && lane < ppt && page0 < seg.q.keys &&
+        (page0 < a.sinks32 || page0 + prow > seg.q.lo)) {
+      const int32_t e = __ldg(a.page_table + (int64_t)seg.b * a.table_stride + lp);
+      if (e >= 0 && e < a.num_pages)
+        row = e << a.page_shift;
+      else if (w == 0)
+        atomicOr(&g_pa_error_flags, kFlagPage);
+    }
+    return row;
+  };
   auto acquire = [&](uint32_t q) -> bool {
     const uint32_t slot = q % NSLOT;
     const bool r_ok = q < (uint32_t)NSLOT ||
@@ -188,23 +229,17 @@ __device__ __forceinline__ void stream_copy_role(const PrefillArgs& a0, const CU
     return r_ok;
   };
   uint32_t base = 0, issued_end = 0;  // fills of the segments before; one past the last issued
-  auto fetch = [&](const PrefillArgs& at, const StreamWalk& seg, int jt) -> int32_t {
-    return tile_page_row<true, true>(at, seg.t0, seg.n, jt, lane, w == 0);
-  };
   StreamWalk s = stream_start(a, run, x0, slots);
-  stream_table(a, a0, s.b);
-  int32_t row_cur = fetch(a, s, 0), row_next = fetch(a, s, 1);
+  int32_t row_cur = fetch(s, 0), row_next = fetch(s, 1);
   for (bool more = true; more && ok;) {
     const int n = s.n;
     // the next segment's first table entries are read a segment ahead
     StreamWalk nx = s;
-    an = a;
-    more = stream_next(an, nx);
+    more = stream_next(a, nx);
     int32_t next_0 = a.oob_row, next_1 = a.oob_row;
     if (more) {
-      stream_table(an, a0, nx.b);
-      next_0 = fetch(an, nx, 0);
-      next_1 = fetch(an, nx, 1);
+      next_0 = fetch(nx, 0);
+      next_1 = fetch(nx, 1);
     }
     int32_t row_prev = a.oob_row;
     for (int j = 0; j <= n && ok; ++j) {
@@ -239,11 +274,10 @@ __device__ __forceinline__ void stream_copy_role(const PrefillArgs& a0, const CU
       }
       row_prev = row_cur;
       row_cur = row_next;
-      row_next = fetch(a, s, j + 2);
+      row_next = fetch(s, j + 2);
     }
     base += 2u * (uint32_t)n * NP;
     s = nx;
-    a = an;
     row_cur = next_0;
     row_next = next_1;
   }
@@ -260,7 +294,7 @@ __device__ __forceinline__ void stream_copy_role(const PrefillArgs& a0, const CU
 template <int D, bool BF16, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
     decode_stream_kernel(const __grid_constant__ CUtensorMap tm_k,
-                         const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a0) {
+                         const __grid_constant__ CUtensorMap tm_v, const PrefillArgs a) {
   using C = StreamCfg<D>;
   constexpr int NP = C::NP, NSLOT = C::NSLOT, NH = D / 128;
   extern __shared__ uint8_t smem_raw[];
@@ -268,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t* run = reinterpret_cast<int64_t*>(smem + C::RUN_OFF);
+  int32_t* run = reinterpret_cast<int32_t*>(smem + C::RUN_OFF);
   auto bar = [&](int i) -> uint32_t { return sb + C::BAR_OFF + 8u * (uint32_t)i; };
   auto slot_addr = [&](uint32_t r) -> uint32_t { return sb + C::RING_OFF + r * kPanel; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF);
@@ -300,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
   }
   tc_fence_before();
   // its barriers also publish the set-up above; `red` is not in use yet
-  stream_scan(a0, run, reinterpret_cast<int64_t*>(smem + C::RED_OFF), blockIdx.x == 0);
+  stream_scan(a, run, reinterpret_cast<int32_t*>(smem + C::RED_OFF), blockIdx.x == 0);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const StreamShare share(run[kStreamRuns], gridDim.x);
@@ -309,10 +343,9 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
     if constexpr (!WHOLE) wait_dependencies();
     return;
   }
-  const int64_t x0 = share.first(blockIdx.x);
-  const int64_t slots = share.first(blockIdx.x + 1) - x0;
-  const uint64_t tmo = a0.timeout_ns;
-  PrefillArgs a = a0;
+  const int32_t x0 = share.first(blockIdx.x);
+  const int32_t slots = share.first(blockIdx.x + 1) - x0;
+  const uint64_t tmo = a.timeout_ns;
 
   if (warp < 4) {
     // ============================================================ softmax + epilogue
@@ -329,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
       for (int i = 0; i < NP / 2; ++i) {
         const int p = t + 128 * i, row = p / (D / 8), col = p % (D / 8);
         qv[i] = row < G ? __ldg(reinterpret_cast<const uint4*>(
-                              a0.q + (b * a.Hq + g * G + row) * (int64_t)D) + col)
+                              a.q + (b * a.Hq + g * G + row) * (int64_t)D) + col)
                         : make_uint4(0u, 0u, 0u, 0u);
       }
     };
@@ -355,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
     q_store(0);
     for (bool more = true; more && ok;) {
       const int n = s.n;
-      const PrefillArgs as = a;  // this segment's sequence; `a` goes on to the next one
+      const StreamSeq seq = s.q;
       StreamWalk nx = s;
       more = stream_next(a, nx);
       if (more) q_load(nx.b, nx.g);
@@ -373,8 +406,8 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
       for (int j = 0; j < n; ++j) {
         const uint32_t i = jj + j;
         const int sbuf = i & 1;
-        const int64_t key0 = kv_tile<true>(as, s.t0 + j) * kTileKeys;
-        const bool live = !key_unseen<true>(as, key0 + t);
+        const int32_t key0 = stream_tile(seq, s.t0 + j) * kTileKeys;
+        const bool live = !stream_unseen(seq, a.sinks32, key0 + t);
         float sv[8];
         if (ok) ok = warp_wait(bar(C::B_SFULL + sbuf), (i >> 1) & 1, abort_flag, tmo);
         if (ok) {
@@ -439,7 +472,8 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
           l_part[h] += p[h];
         }
         if (ok && i >= 2) ok = wait_pv(i - 2);  // the last reader of P's buffer
-        if (ok && tile_unseen<true>(as, key0)) {
+        if (ok && (key0 + kTileKeys > seq.keys ||
+                   max(key0, a.sinks32) < min(key0 + kTileKeys, seq.lo))) {
           // V rows of keys that the row does not see may hold any bits; P is 0 there, but
           // 0 * NaN is NaN inside the MMA, so those rows are zeroed. Once S(j+1) and PV(i-1)
           // are done, every earlier fill of V(j)'s slots has landed (K up to K(j+1), V up to
@@ -452,7 +486,9 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
           for (int q = 0; q < NP && ok; ++q)
             ok = warp_wait(bar(C::B_FULL + (seq0 + q) % NSLOT), ((seq0 + q) / NSLOT) & 1,
                            abort_flag, tmo);
-          if (ok && v_row_unclean<true>(as, key0 + t)) {
+          const int32_t page0 = (key0 + t) & ~(a.page_rows - 1);  // its page's first key
+          if (ok && !live && page0 < seq.keys &&  // (pages not loaded arrived as zeros)
+              (page0 < a.sinks32 || page0 + a.page_rows > seq.lo)) {
 #pragma unroll
             for (int q = 0; q < NP; ++q) {
               const uint32_t off = v_offset<NP, C::PANEL_LOG>((uint32_t)t, q, a.v_shift);
@@ -498,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
         inv_l[h] = ls[h] > 0.f ? __frcp_rn(ls[h]) : 0.f;
       }
       const bool whole = n == s.n_b;
-      const int64_t out_row = s.b * a.Hq + s.g * G;  // heads g G .. g G + G - 1
+      const int64_t out_row = (int64_t)s.b * a.Hq + s.g * G;  // heads g G .. g G + G - 1
       const int64_t row0 =
           whole ? out_row
                 : (WHOLE ? 0 : (int64_t)a.batch * a.Hq) +
@@ -536,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
     }
   } else if (warp > kMmaWarp) {
     // ============================================================ TMA issuers (three warps)
-    stream_copy_role<NP, NSLOT, C::PANEL_LOG>(a0, &tm_k, &tm_v, run, x0, slots,
+    stream_copy_role<NP, NSLOT, C::PANEL_LOG>(a, &tm_k, &tm_v, run, x0, slots,
                                               warp - kMmaWarp - 1, sb + C::RING_OFF,
                                               bar(C::B_FULL), bar(C::B_EMPTY), abort_flag, tmo);
   } else {
@@ -648,38 +684,39 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
 constexpr int kMergeWarps = kStreamRuns / 32;
 
 template <int D, int OUT, bool PREFIX, int WPR>
-__global__ void __launch_bounds__(kStreamRuns, WPR > 1 ? 4 : 1) merge_stream_kernel(const PrefillArgs a0,
+__global__ void __launch_bounds__(kStreamRuns, WPR > 1 ? 4 : 1) merge_stream_kernel(const PrefillArgs a,
                                                                    int64_t grid_ctas,
                                                                    const float* pre_o,
                                                                    const float* pre_lse,
                                                                    int n_pre) {
   static_assert(WPR == 1 || WPR == kMergeWarps, "a row takes a warp or the block");
   constexpr int NV = D / 128;  // float4 columns a lane holds
-  __shared__ int64_t run[kStreamRuns + 1], wsum[kMergeWarps];
+  __shared__ int32_t run[kStreamRuns + 1], wsum[kMergeWarps];
   __shared__ float wpart[WPR > 1 ? kMergeWarps : 1][2];               // M and W of a warp's parts
   __shared__ float4 opart[WPR > 1 ? kMergeWarps : 1][NV][32];         // their weighted rows
-  stream_scan(a0, run, wsum, false);
+  stream_scan(a, run, wsum, false);
   // Launched while the stream kernel ends (programmatic launch): its results are complete past
   // this wait. The lengths above were there before it.
   wait_dependencies();
   const StreamShare share(run[kStreamRuns], grid_ctas);
   const int lane = threadIdx.x & 31, wid = threadIdx.x / 32;
-  const int64_t rows = (int64_t)a0.batch * a0.Hq;
-  const int per = stream_per(a0);
-  PrefillArgs a = a0;
+  const int64_t rows = (int64_t)a.batch * a.Hq;
+  const int32_t per = stream_per(a);
   const int first = WPR > 1 ? wid : 0;  // this warp's first part
   constexpr int64_t kRows = kMergeWarps / WPR;  // rows of a block
   for (int64_t row = (int64_t)blockIdx.x * kRows + wid / WPR; row < rows;
        row += (int64_t)gridDim.x * kRows) {
-    const int64_t b = div_pos(row, a.Hq), in_run = div_pos(b, per);
-    const int head = (int)(row - b * a.Hq), g = head / a.G;
+    // rows < 2^31 (as the sequences' Q tiles are counted in 32 bits)
+    const int32_t b = (int32_t)((uint32_t)row / (uint32_t)a.Hq), in_run = b / per;
+    const int head = (int)(row - (int64_t)b * a.Hq), g = head / a.G;
     bool bad;
-    int64_t off = run[in_run];  // the unit's first slot (its start; its tiles follow)
-    for (int64_t c = in_run * per; c < b; ++c)
-      off += stream_slots(stream_seq(a, c, &bad)) * a.Hkv;
-    const int64_t n_b = stream_seq(a, b, &bad);
+    StreamSeq q;
+    int32_t off = run[in_run];  // the unit's first slot (its start; its tiles follow)
+    for (int32_t c = in_run * per; c < b; ++c)
+      off += stream_slots(stream_seq(a, c, q, &bad)) * a.Hkv;
+    const int32_t n_b = stream_seq(a, b, q, &bad);
     off += g * (n_b + 1);
-    int64_t c0 = 0, np = 0;  // parts of the unit
+    int32_t c0 = 0, np = 0;  // parts of the unit
     bool whole = false, late = false;
     if (n_b > 0) {
       c0 = share.owner(off + 1);

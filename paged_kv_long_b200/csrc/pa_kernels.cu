@@ -105,6 +105,8 @@ struct PrefillArgs {
   int64_t window, sinks;
   int64_t win_lo, tile_head, tile_gap;
   int64_t first_key;       // WIN: keys below it are not this launch's (a shared prefix's)
+  int32_t seq_cap;         // keys that a table row can map, below 2^31 - 2 tiles (stream kernel)
+  int32_t window32, sinks32, first_key32;
 };
 
 // KV tile of entry t of the unit's tile list.
@@ -701,28 +703,6 @@ __device__ __forceinline__ int32_t tile_page_row(const PrefillArgs& a, int64_t k
   return row;
 }
 
-// The keys of sequence b (clamped into the table row; *bad: they were outside) and its tile list,
-// set in a: total_keys, win_lo, tile_head, tile_gap. Returns the number of tiles.
-__device__ __forceinline__ int64_t stream_seq(PrefillArgs& a, int64_t b, bool* bad) {
-  int64_t len = __ldg(a.seq_lens + b);
-  const int64_t cap = (int64_t)a.table_stride * a.page_rows;
-  if (len < 0 || len > cap) {
-    *bad = true;
-    len = len < 0 ? 0 : cap;
-  }
-  a.total_keys = len;
-  if (len <= a.first_key) return 0;
-  int64_t n;
-  a.win_lo = window_lo(len - 1, a.window);
-  if (a.first_key > a.win_lo) a.win_lo = a.first_key;
-  const int64_t w0 = a.win_lo / kTileKeys;
-  const int64_t hs = ceil_div64(a.sinks < len ? a.sinks : len, kTileKeys);
-  a.tile_head = hs;
-  a.tile_gap = hs < w0 ? w0 - hs : 0;
-  n = (len - 1) / kTileKeys + 1 - a.tile_gap;
-  return n;
-}
-
 // Device-length decode, block blockIdx.x: unit (sequence of rank blockIdx.x / (Hkv·S), KV head
 // g, split s) over its keys 0 .. len-1 (the new token's own included, all visible). Points a at
 // the sequence (Q, output and workspace rows, page-table row, lengths) and gives the unit's KV
@@ -748,7 +728,6 @@ __device__ __forceinline__ void decode_unit(PrefillArgs& a, int32_t* scratch, in
     if (threadIdx.x == 0 && *g == 0 && *s == 0) atomicOr(&g_pa_error_flags, kFlagPage);
     len = len < 0 ? 0 : cap;
   }
-  const int64_t seq = b;
   a.q += b * a.Hq * D;
   a.out = out_at<WIN>(a.out, b * a.Hq * D);
   if (a.ws_o) {
@@ -761,8 +740,16 @@ __device__ __forceinline__ void decode_unit(PrefillArgs& a, int32_t* scratch, in
   a.table_len = (len + a.page_rows - 1) / a.page_rows;
   a.R = len > 0 ? 1 : 0;
   if constexpr (WIN) {
-    bool bad;
-    split_range(stream_seq(a, seq, &bad), *s, a.splits, kt0, kt1);
+    int64_t n = 0;
+    if (len > a.first_key) {
+      a.win_lo = window_lo(len - 1, a.window);
+      if (a.win_lo < a.first_key) a.win_lo = a.first_key;
+      const int64_t w0 = a.win_lo / kTileKeys;
+      a.tile_head = ceil_div64(a.sinks < len ? a.sinks : len, kTileKeys);
+      a.tile_gap = a.tile_head < w0 ? w0 - a.tile_head : 0;
+      n = (len - 1) / kTileKeys + 1 - a.tile_gap;
+    }
+    split_range(n, *s, a.splits, kt0, kt1);
     return;
   }
   split_range((len + kTileKeys - 1) / kTileKeys, *s, a.splits, kt0, kt1);
@@ -1461,6 +1448,24 @@ cudaError_t launch_decode_d(int D, bool bf16, int64_t grid, cudaStream_t st,
 // overlaps the stream kernel's end). a.ws_o / ws_lse: the rows of the stream kernel's partials.
 // PREFIX: every unit leaves a partial, and n_pre partials of the prefix join (see the kernels);
 // the stream kernel's launch overlaps the prefix's kernel before it.
+// The stream kernel's 32-bit view of a window or a first key. False when its slots could pass 2^31.
+bool stream_args(PrefillArgs& a, int64_t window, int64_t sinks, int64_t first_key) {
+  const int64_t most = (int64_t(1) << 31) - 1 - 2 * kTileKeys;
+  a.window = window;
+  a.sinks = sinks;
+  a.first_key = first_key;
+  a.seq_cap = (int32_t)std::min((int64_t)a.table_stride * a.page_rows, most);
+  a.window32 = (int32_t)std::min(window, most);
+  a.sinks32 = (int32_t)std::min(sinks, most);
+  a.first_key32 = (int32_t)std::min(first_key, most);
+  const int64_t tiles = std::max<int64_t>(
+      1, std::min(window_most_tiles(a.seq_cap, window, sinks),
+                  ceil_div64(std::max<int64_t>(a.seq_cap - first_key, 0), kTileKeys) + 1 +
+                      ceil_div64(sinks, kTileKeys)));
+  return (double)a.batch * a.Hkv * (double)(tiles + 1) < 2147483648.0 &&
+         (double)a.batch * a.Hq < 2147483648.0;
+}
+
 template <int D, bool BF16, bool PREFIX>
 cudaError_t launch_stream(int64_t ctas, cudaStream_t st, const CUtensorMap& tk,
                           const CUtensorMap& tv, const PrefillArgs& a, const float* pre_o,
@@ -1779,8 +1784,7 @@ extern "C" int pa_window_decode(const pa_plan_t* plan, int window, int n_sinks, 
                              num_pages, out, &tk, &tv, &a);
   if (st != PA_OK) return st;
   const bool bf16 = plan->dtype == PA_BF16;
-  a.window = window;
-  a.sinks = n_sinks;
+  if (!stream_args(a, window, n_sinks, 0)) return PA_ERR_UNSUPPORTED;
   a.splits = w.splits;
   a.ws_o = plan->ws_bytes > 0 ? lse_ws : nullptr;
   a.ws_lse = plan->ws_bytes > 0 ? lse_ws + w.ws_rows(G, rows) * D : nullptr;
@@ -1871,9 +1875,7 @@ extern "C" int pa_prefix_decode(const pa_plan_t* plan, int64_t prefix_len, const
   if (e != cudaSuccess) return PA_ERR_CUDA;
 
   // Every sequence's own keys, from the prefix's end on, and the merge of all partials.
-  a.window = int64_t(1) << 40;
-  a.sinks = 0;
-  a.first_key = prefix_len;
+  if (!stream_args(a, int64_t(1) << 40, 0, prefix_len)) return PA_ERR_UNSUPPORTED;
   a.ws_o = lse_ws + (int64_t)w.splits * rows * D;
   a.ws_lse = lse + (int64_t)w.splits * rows;
   if (w.own.stream) {
