@@ -502,16 +502,31 @@ def batch_prefill(bp: BatchPlan, q, k_pool, v_pool, block_table, out=None, ws=No
     return out
 
 
-class WindowPlan:
+class _StepPlan:
+    """A plan whose fields the calls of every step and layer need, read out of it once."""
+
+    def __init__(self, plan: Plan):
+        self.plan = plan
+        self.ref = ctypes.byref(plan)
+        self.torch_dtype = _torch_dtype(plan)
+        self.q_shape = (plan.chunk_rows, plan.n_q_heads, plan.head_dim)
+        self.page_shape = (plan.page_size, plan.n_kv_heads, plan.head_dim)
+        self.batch = plan.batch
+        self.ws_numel = plan.ws_bytes // 4
+
+
+class WindowPlan(_StepPlan):
     """A plan with its window and sinks (pa_window_plan with the host length arrays it was made
     from, or pa_window_decode_plan without)."""
 
     def __init__(self, plan: Plan, window: int, n_sinks: int, q_lens=None, hist_lens=None):
-        self.plan = plan
+        super().__init__(plan)
         self.window = window
         self.n_sinks = n_sinks
         self.q_lens = q_lens
         self.hist_lens = hist_lens
+        if q_lens is not None:
+            self.lens_ptrs = (q_lens.ctypes.data, hist_lens.ctypes.data)
 
 
 def _num_sms() -> int:
@@ -539,8 +554,8 @@ def window_plan(n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, 
     if q_lens.shape != hist_lens.shape or q_lens.ndim != 1:
         raise ValueError("q_lens and hist_lens must be 1-D of the same length")
     p = Plan()
-    st = load_library().pa_window_plan(num_sms or _num_sms(), n_q_heads, n_kv_heads, head_dim,
-                                       page_size, len(q_lens), q_lens.ctypes.data,
+    st = load_library().pa_window_plan(_num_sms() if num_sms is None else num_sms, n_q_heads,
+                                       n_kv_heads, head_dim, page_size, len(q_lens), q_lens.ctypes.data,
                                        hist_lens.ctypes.data, window, n_sinks,
                                        _dtype_code(dtype), scale, ctypes.byref(p))
     _check(st, "pa_window_plan")
@@ -571,9 +586,9 @@ def window_decode_plan(n_q_heads: int, n_kv_heads: int, head_dim: int, page_size
     sinks (host only)."""
     window, n_sinks = _window_args(window, n_sinks)
     p = Plan()
-    st = load_library().pa_window_decode_plan(num_sms or _num_sms(), n_q_heads, n_kv_heads,
-                                              head_dim, page_size, batch, max_seq_len, window,
-                                              n_sinks, _dtype_code(dtype), scale,
+    st = load_library().pa_window_decode_plan(_num_sms() if num_sms is None else num_sms,
+                                              n_q_heads, n_kv_heads, head_dim, page_size, batch,
+                                              max_seq_len, window, n_sinks, _dtype_code(dtype), scale,
                                               ctypes.byref(p))
     _check(st, "pa_window_decode_plan")
     return WindowPlan(p, window, n_sinks)
@@ -626,34 +641,33 @@ def _used_on(stream, *tensors):
             t.record_stream(stream)
 
 
-def _step_tensors(p: Plan, rows, q, k_pool, v_pool, block_table, out, ws, stream, device):
-    """Checks of the tensors that the window and prefix calls take; (out, ws, its pointer, its bytes)."""
+def _step_tensors(sp: _StepPlan, q, k_pool, v_pool, block_table, out, ws, stream, device):
+    """Checks of the tensors that the window and prefix calls take; (out, ws, its pointer, its
+    bytes)."""
     import torch
-    dt = _torch_dtype(p)
-    D = p.head_dim
-    heads = (rows, p.n_q_heads, D)
-    _require(q, "q", dt, heads, device)
+    dt = sp.torch_dtype
+    _require(q, "q", dt, sp.q_shape, device)
     _require(k_pool, "k_pool", dt, None, device)
     pool = k_pool.shape
-    if len(pool) != 4 or pool[1:] != (p.page_size, p.n_kv_heads, D):
+    if len(pool) != 4 or pool[1:] != sp.page_shape:
         raise ValueError("k_pool must be [num_pages, page_size, Hkv, D]")
     _require(v_pool, "v_pool", dt, pool, device)
     _require(block_table, "block_table", torch.int32, None, device)
-    if block_table.dim() != 2 or block_table.shape[0] != p.batch:
+    if block_table.dim() != 2 or block_table.shape[0] != sp.batch:
         raise ValueError("block_table must be [batch, max_pages]")
     if out is None:
         out = torch.empty_like(q)
         _used_on(stream, out)
     else:
-        _require(out, "out", dt, heads, device)
-    if p.ws_bytes == 0:
+        _require(out, "out", dt, sp.q_shape, device)
+    if sp.ws_numel == 0:
         return out, None, None, 0
     if ws is None:
-        ws = torch.empty(p.ws_bytes // 4, dtype=torch.float32, device=q.device)
+        ws = torch.empty(sp.ws_numel, dtype=torch.float32, device=q.device)
         _used_on(stream, ws)
-    else:
-        _require(ws, "ws", torch.float32, None, device)
-    return out, ws, ws.data_ptr(), ws.numel() * 4
+        return out, ws, ws.data_ptr(), 4 * sp.ws_numel
+    _require(ws, "ws", torch.float32, None, device)
+    return out, ws, ws.data_ptr(), 4 * ws.numel()
 
 
 def window_decode(wp: WindowPlan, q, k_pool, v_pool, block_table, seq_lens, out=None, ws=None,
@@ -662,15 +676,13 @@ def window_decode(wp: WindowPlan, q, k_pool, v_pool, block_table, seq_lens, out=
     `n_sinks` of that sequence (see include/pa.h). q [B, Hq, D]; block_table int32
     [B, max_pages]; seq_lens int32 [B]. Returns out [B, Hq, D] of q's type."""
     import torch
-    p = wp.plan
     if wp.q_lens is not None:
         raise ValueError("a plan of window_plan runs with window_prefill")
     device = _device_of(q, "q")
-    _require(seq_lens, "seq_lens", torch.int32, (p.batch,), device)
-    out, ws, ws_ptr, ws_bytes = _step_tensors(p, p.batch, q, k_pool, v_pool, block_table, out,
-                                                ws, stream, device)
-    _call(device, stream, load_library().pa_window_decode, "pa_window_decode",
-          ctypes.byref(p), wp.window, wp.n_sinks, q.data_ptr(), k_pool.data_ptr(),
+    _require(seq_lens, "seq_lens", torch.int32, (wp.batch,), device)
+    out, ws, ws_ptr, ws_bytes = _step_tensors(wp, q, k_pool, v_pool, block_table, out, ws, stream,
+                                              device)
+    _call(device, stream, load_library().pa_window_decode, "pa_window_decode", wp.ref, wp.window, wp.n_sinks, q.data_ptr(), k_pool.data_ptr(),
           v_pool.data_ptr(), block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(),
           k_pool.shape[0], out.data_ptr(), ws_ptr, ws_bytes)
     return out
@@ -680,24 +692,22 @@ def window_prefill(wp: WindowPlan, q, k_pool, v_pool, block_table, out=None, ws=
     """pa_window_prefill: the chunks of a batch under the plan's sliding window and sinks (see
     include/pa.h). q [sum q_lens, Hq, D] packed in order; block_table int32 [batch, max_pages].
     Returns out [sum q_lens, Hq, D] of q's type."""
-    p = wp.plan
     if wp.q_lens is None:
         raise ValueError("a plan of window_decode_plan runs with window_decode")
     device = _device_of(q, "q")
-    out, ws, ws_ptr, ws_bytes = _step_tensors(p, p.chunk_rows, q, k_pool, v_pool, block_table,
-                                                out, ws, stream, device)
-    _call(device, stream, load_library().pa_window_prefill, "pa_window_prefill",
-          ctypes.byref(p), wp.q_lens.ctypes.data, wp.hist_lens.ctypes.data, wp.window, wp.n_sinks,
-          q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(),
+    out, ws, ws_ptr, ws_bytes = _step_tensors(wp, q, k_pool, v_pool, block_table, out, ws, stream,
+                                              device)
+    _call(device, stream, load_library().pa_window_prefill, "pa_window_prefill", wp.ref,
+          *wp.lens_ptrs, wp.window, wp.n_sinks, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(),
           block_table.shape[1], k_pool.shape[0], out.data_ptr(), ws_ptr, ws_bytes)
     return out
 
 
-class PrefixPlan:
+class PrefixPlan(_StepPlan):
     """A plan of pa_prefix_decode_plan with its prefix length."""
 
     def __init__(self, plan: Plan, prefix_len: int):
-        self.plan = plan
+        super().__init__(plan)
         self.prefix_len = prefix_len
 
 
@@ -707,8 +717,9 @@ def prefix_decode_plan(n_q_heads: int, n_kv_heads: int, head_dim: int, page_size
     """pa_prefix_decode_plan: launch and workspace of a decode step over a shared prefix (host
     only)."""
     p = Plan()
-    st = load_library().pa_prefix_decode_plan(num_sms or _num_sms(), n_q_heads, n_kv_heads,
-                                              head_dim, page_size, batch, prefix_len, max_seq_len,
+    st = load_library().pa_prefix_decode_plan(_num_sms() if num_sms is None else num_sms,
+                                              n_q_heads, n_kv_heads, head_dim, page_size, batch,
+                                              prefix_len, max_seq_len,
                                               _dtype_code(dtype), scale, ctypes.byref(p))
     _check(st, "pa_prefix_decode_plan")
     return PrefixPlan(p, prefix_len)
@@ -721,14 +732,14 @@ def prefix_decode(pp: PrefixPlan, q, k_pool, v_pool, prefix_table, block_table, 
     block_table int32 [B, max_pages] and seq_lens int32 [B] of whole sequences. Returns out
     [B, Hq, D] of q's type."""
     import torch
-    p = pp.plan
     device = _device_of(q, "q")
-    _require(prefix_table, "prefix_table", torch.int32, (pp.prefix_len // p.page_size,), device)
-    _require(seq_lens, "seq_lens", torch.int32, (p.batch,), device)
-    out, ws, ws_ptr, ws_bytes = _step_tensors(p, p.batch, q, k_pool, v_pool, block_table, out,
-                                                ws, stream, device)
-    _call(device, stream, load_library().pa_prefix_decode, "pa_prefix_decode",
-          ctypes.byref(p), pp.prefix_len, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+    _require(prefix_table, "prefix_table", torch.int32, (pp.prefix_len // pp.page_shape[0],),
+             device)
+    _require(seq_lens, "seq_lens", torch.int32, (pp.batch,), device)
+    out, ws, ws_ptr, ws_bytes = _step_tensors(pp, q, k_pool, v_pool, block_table, out, ws, stream,
+                                              device)
+    _call(device, stream, load_library().pa_prefix_decode, "pa_prefix_decode", pp.ref,
+          pp.prefix_len, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
           prefix_table.data_ptr(), block_table.data_ptr(), block_table.shape[1],
           seq_lens.data_ptr(), k_pool.shape[0], out.data_ptr(), ws_ptr, ws_bytes)
     return out
