@@ -42,7 +42,8 @@ typedef enum {
   PA_ERR_INVALID_ARG = -1,  /* null/misaligned pointer, inconsistent sizes, plan mismatch */
   PA_ERR_UNSUPPORTED = -2,  /* shape outside the supported set (see pa_plan) */
   PA_ERR_WORKSPACE = -3,    /* lse_ws missing or smaller than plan->ws_bytes */
-  PA_ERR_CUDA = -4,         /* a CUDA runtime/driver call failed (launch, tensor map, ...) */
+  PA_ERR_CUDA = -4,         /* a CUDA runtime/driver call failed (launch, tensor map, ...), or
+                             * host memory ran out */
   PA_ERR_TIMEOUT = -5,      /* a kernel wait gave up (reported by pa_device_error) */
   PA_ERR_PAGE_INDEX = -6    /* a page-table entry was outside [0, num_pages) */
 } pa_status;
@@ -293,7 +294,9 @@ int pa_batch_combine(const pa_plan_t* plan, const int32_t* q_lens, const int64_t
  * page). Any other slot that no row of the launch sees may hold any bits, NaN included. A
  * non-finite key or value that some row does see may reach other rows of the same sequence (rows
  * share key tiles).
- *   out has the type of q: the sums are fp32, split partials too, and the row is rounded once.
+ *   out has the type of q: the sums are fp32, split partials too, and the row is rounded once. It
+ * may not overlap q. Calls that may overlap on the GPU (other streams, other captured graphs)
+ * need workspaces of their own.
  * Softmax and products are those of pa_prefill (probabilities rounded to the input type).
  * The pages have no counterpart; it is the attention of models whose local layers see a window,
  * and of caches bounded to a window and the first tokens.
@@ -330,6 +333,8 @@ int pa_window_schedule_items(const pa_plan_t* plan, const int32_t* q_lens,
  * the lengths on the device are; the others in uniform splits (plan->splits). The plan's policy is
  * PA_POLICY_WINDOW_DECODE and its hist_len max_seq_len, which only sizes the launch: longer
  * sequences are right too. `window` and `n_sinks` must be those it was made with.
+ * PA_ERR_UNSUPPORTED: batch * Hkv * (the most KV tiles a table row and the window reach, plus one)
+ * or batch * Hq passes 2^31.
  */
 int pa_window_decode_plan(int num_sms, int n_q_heads, int n_kv_heads, int head_dim, int page_size,
                           int batch, int64_t max_seq_len, int window, int n_sinks, int dtype,
@@ -438,6 +443,8 @@ int pa_kv_publish(int n_kv_heads, int head_dim, int page_size, int dtype, const 
  *   free_pages         device int32 [n_free]: pages in no table row; taken in order.
  *   pages_used         device int32 [1]: entries of free_pages that earlier steps took;
  *   pages_used_out     device int32 [1], not the same word: that plus the pages taken here.
+ *                      (No output may overlap an input: nothing is updated in place but
+ *                      block_table.)
  *   block_table        device int32 [batch][table_stride], updated in place: request b owns
  *                      entries 0 .. ceil(h/PS)-1 (only read) and gets the entries up to
  *                      ceil((h+r)/PS)-1 from the free list, request by request. Others stay.

@@ -549,8 +549,8 @@ def window_plan(n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, 
     only; one sequence is a batch of one)."""
     import numpy as np
     window, n_sinks = _window_args(window, n_sinks)
-    q_lens = np.ascontiguousarray(q_lens, dtype=np.int32)
-    hist_lens = np.ascontiguousarray(hist_lens, dtype=np.int64)
+    q_lens = np.array(q_lens, dtype=np.int32)  # copies: the plan's own
+    hist_lens = np.array(hist_lens, dtype=np.int64)
     if q_lens.shape != hist_lens.shape or q_lens.ndim != 1:
         raise ValueError("q_lens and hist_lens must be 1-D of the same length")
     p = Plan()

@@ -2108,18 +2108,20 @@ extern "C" int pa_window_prefill(const pa_plan_t* plan, const int32_t* q_lens,
                                  void* out, float* lse_ws, uint64_t ws_bytes,
                                  pa_stream_t stream) {
   if (window < 1 || n_sinks < 0) return PA_ERR_INVALID_ARG;
-  const Window win{window, n_sinks};
-  Batch bt;
-  Schedule sch;
-  int st = rebuild_batch(plan, &win, q_lens, hist_lens, &bt, &sch);
-  if (st != PA_OK) return st;
-  float* o = static_cast<float*>(out);
-  st = run_batch(plan, &win, bt, sch, q, k_pool, v_pool, block_table, table_stride, num_pages, o,
-                 lse_ws, ws_bytes, stream);
-  if (st != PA_OK) return st;
-  return plan->dtype == PA_BF16
-             ? merge_batch<kOutBf16>(plan, bt, sch, lse_ws, ws_bytes, o, stream)
-             : merge_batch<kOutF16>(plan, bt, sch, lse_ws, ws_bytes, o, stream);
+  return no_throw([&] {
+    const Window win{window, n_sinks};
+    Batch bt;
+    Schedule sch;
+    int st = rebuild_batch(plan, &win, q_lens, hist_lens, &bt, &sch);
+    if (st != PA_OK) return st;
+    float* o = static_cast<float*>(out);
+    st = run_batch(plan, &win, bt, sch, q, k_pool, v_pool, block_table, table_stride, num_pages,
+                   o, lse_ws, ws_bytes, stream);
+    if (st != PA_OK) return st;
+    return plan->dtype == PA_BF16
+               ? merge_batch<kOutBf16>(plan, bt, sch, lse_ws, ws_bytes, o, stream)
+               : merge_batch<kOutF16>(plan, bt, sch, lse_ws, ws_bytes, o, stream);
+  });
 }
 
 // ---------------------------------------------------------------- entry point without allocation
@@ -2213,7 +2215,10 @@ extern "C" int pa_block_tables(int batch, const int32_t* q_lens, const int32_t* 
   if (!q_lens || !hist_lens || !pages_used || !pages_used_out || !block_table || !cu_q_lens ||
       !seq_lens || (n_free > 0 && !free_pages) || (max_rows > 0 && (!slots || !positions)))
     return PA_ERR_INVALID_ARG;
-  if (pages_used == pages_used_out) return PA_ERR_INVALID_ARG;  // other blocks still read it
+  // every block reads the inputs while the first ones already write: nothing in place
+  for (const int32_t* out : {pages_used_out, block_table, slots, positions, cu_q_lens, seq_lens})
+    if (out && (out == q_lens || out == hist_lens || out == free_pages || out == pages_used))
+      return PA_ERR_INVALID_ARG;
   if (page_size < 16 || page_size > 128 || (page_size & (page_size - 1))) return PA_ERR_UNSUPPORTED;
   if (batch > kStepMaxSeqs || num_pages >= ((int64_t(1) << 31) - kTileKeys) / page_size)
     return PA_ERR_UNSUPPORTED;
@@ -2268,6 +2273,7 @@ extern "C" int pa_qk_rope_append(int n_q_heads, int n_kv_heads, int head_dim, in
   if (!q || !k || !v || !positions || !slots || !rope || !q_out || !k_pool || !v_pool)
     return PA_ERR_INVALID_ARG;
   const int64_t qw = (int64_t)n_q_heads * head_dim, kw = (int64_t)n_kv_heads * head_dim;
+  if (q == q_out && q_stride != qw) return PA_ERR_INVALID_ARG;  // in place: the same rows
   if (q_stride < qw || k_stride < kw || v_stride < kw || q_stride % 8 || k_stride % 8 ||
       v_stride % 8)
     return PA_ERR_INVALID_ARG;

@@ -469,8 +469,10 @@ extern "C" int pa_window_plan(int num_sms, int n_q_heads, int n_kv_heads, int he
   memset(plan, 0, sizeof *plan);
   if (window < 1 || n_sinks < 0) return PA_ERR_INVALID_ARG;
   const pa::Window win{window, n_sinks};
-  return plan_batch(num_sms, n_q_heads, n_kv_heads, head_dim, page_size, batch, q_lens, hist_lens,
-                    &win, dtype, scale, plan);
+  return pa::no_throw([&] {
+    return plan_batch(num_sms, n_q_heads, n_kv_heads, head_dim, page_size, batch, q_lens,
+                      hist_lens, &win, dtype, scale, plan);
+  });
 }
 
 namespace pa {
@@ -801,7 +803,7 @@ extern "C" int pa_window_schedule_items(const pa_plan_t* plan, const int32_t* q_
                                         int32_t* items, int cap) {
   if (window < 1 || n_sinks < 0) return PA_ERR_INVALID_ARG;
   const pa::Window win{window, n_sinks};
-  return batch_items(plan, q_lens, hist_lens, &win, items, cap);
+  return pa::no_throw([&] { return batch_items(plan, q_lens, hist_lens, &win, items, cap); });
 }
 
 extern "C" int pa_schedule_items(const pa_plan_t* plan, int32_t* items, int cap) {

@@ -9,6 +9,16 @@
 
 namespace pa {
 
+// f's status; PA_ERR_CUDA when host memory runs out (nothing throws across the ABI).
+template <class F>
+int no_throw(F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    return PA_ERR_CUDA;
+  }
+}
+
 struct Schedule {
   std::vector<PaItem> items;          // in launch order
   std::vector<PaSplitBlock> split;    // row blocks with more than one item

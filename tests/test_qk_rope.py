@@ -178,6 +178,8 @@ def test_refusals():
     assert call(Hq=0) == call(Hkv=0) == call(dtype=2) == call(rows=-1) == call(max_pos=0) == bad
     assert call(pages=0) == call(q=None) == call(slots=None) == call(rope=None) == bad
     assert call(q=odd) == call(qw=odd) == call(kp=odd) == call(out=odd) == bad
+    assert call(qs=520) == bad                # q_out is q: its rows must be q_out's
+    assert call(out=ctypes.c_void_p(1 << 21), qs=520, rows=0) == "PA_OK"
     assert call(qs=504) == call(ks=260) == call(vs=248) == bad  # short or not a multiple of 8
     assert call(eps=-1.0) == call(eps=float("nan")) == call(eps=float("inf")) == bad
     assert call(D=96) == call(PS=24) == call(rot=8) == call(rot=144) == call(rot=24) == uns

@@ -135,8 +135,8 @@ def test_refusals():
     lib, bd = _binding().load_library(), _binding()
     p, q = ctypes.c_void_p(1 << 20), ctypes.c_void_p(1 << 21)
 
-    def call(batch=2, q_lens=p, ps=16, pages=10, free=p, n_free=4, used=p, used_out=q, table=p,
-             stride=4, rows=8, slots=p, pos=p, cu=p, seq=p):
+    def call(batch=2, q_lens=p, ps=16, pages=10, free=p, n_free=4, used=p, used_out=q, table=q,
+             stride=4, rows=8, slots=q, pos=q, cu=q, seq=q):
         return bd.STATUS[lib.pa_block_tables(batch, q_lens, p, ps, pages, free, n_free, used,
                                              used_out, table, stride, rows, slots, pos, cu, seq,
                                              None)]
@@ -145,7 +145,8 @@ def test_refusals():
     assert call(batch=0) == bad and call(q_lens=None) == bad and call(pages=0) == bad
     assert call(free=None) == bad and call(n_free=-1) == bad and call(table=None) == bad
     assert call(stride=0) == bad and call(rows=-1) == bad and call(slots=None) == bad
-    assert call(used_out=p) == bad  # the counter is read by every block: not in place
+    # every block reads the inputs while others write: nothing in place
+    assert call(used_out=p) == call(seq=p) == call(slots=p) == call(table=p) == bad
     assert call(ps=24) == call(ps=8) == call(ps=256) == "PA_ERR_UNSUPPORTED"
     assert call(batch=4097) == "PA_ERR_UNSUPPORTED"
     assert call(pages=1 << 27) == "PA_ERR_UNSUPPORTED"  # 2^31 slots

@@ -341,6 +341,15 @@ def test_refusals():
     assert prefill(wp) == bad
 
 
+def test_plan_keeps_its_own_lengths():
+    bd = _binding()
+    rows, hist = np.array([3, 5], np.int32), np.array([9, 0], np.int64)
+    wp = bd.window_plan(4, 2, 64, 16, rows, hist, 4, num_sms=148)
+    rows += 100
+    hist += 100
+    assert wp.q_lens.tolist() == [3, 5] and wp.hist_lens.tolist() == [9, 0]
+
+
 def test_binding_refuses_the_other_plan():
     bd = _binding()
     wd = bd.window_decode_plan(16, 2, 256, 16, 4, 1000, 200, 4, "f16", num_sms=148)
