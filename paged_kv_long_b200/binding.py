@@ -555,8 +555,8 @@ def window_plan(n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, 
         raise ValueError("q_lens and hist_lens must be 1-D of the same length")
     p = Plan()
     st = load_library().pa_window_plan(_num_sms() if num_sms is None else num_sms, n_q_heads,
-                                       n_kv_heads, head_dim, page_size, len(q_lens), q_lens.ctypes.data,
-                                       hist_lens.ctypes.data, window, n_sinks,
+                                       n_kv_heads, head_dim, page_size, len(q_lens),
+                                       q_lens.ctypes.data, hist_lens.ctypes.data, window, n_sinks,
                                        _dtype_code(dtype), scale, ctypes.byref(p))
     _check(st, "pa_window_plan")
     return WindowPlan(p, window, n_sinks, q_lens, hist_lens)
@@ -588,8 +588,8 @@ def window_decode_plan(n_q_heads: int, n_kv_heads: int, head_dim: int, page_size
     p = Plan()
     st = load_library().pa_window_decode_plan(_num_sms() if num_sms is None else num_sms,
                                               n_q_heads, n_kv_heads, head_dim, page_size, batch,
-                                              max_seq_len, window, n_sinks, _dtype_code(dtype), scale,
-                                              ctypes.byref(p))
+                                              max_seq_len, window, n_sinks, _dtype_code(dtype),
+                                              scale, ctypes.byref(p))
     _check(st, "pa_window_decode_plan")
     return WindowPlan(p, window, n_sinks)
 
@@ -682,9 +682,10 @@ def window_decode(wp: WindowPlan, q, k_pool, v_pool, block_table, seq_lens, out=
     _require(seq_lens, "seq_lens", torch.int32, (wp.batch,), device)
     out, ws, ws_ptr, ws_bytes = _step_tensors(wp, q, k_pool, v_pool, block_table, out, ws, stream,
                                               device)
-    _call(device, stream, load_library().pa_window_decode, "pa_window_decode", wp.ref, wp.window, wp.n_sinks, q.data_ptr(), k_pool.data_ptr(),
-          v_pool.data_ptr(), block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(),
-          k_pool.shape[0], out.data_ptr(), ws_ptr, ws_bytes)
+    _call(device, stream, load_library().pa_window_decode, "pa_window_decode", wp.ref, wp.window,
+          wp.n_sinks, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(),
+          block_table.shape[1], seq_lens.data_ptr(), k_pool.shape[0], out.data_ptr(), ws_ptr,
+          ws_bytes)
     return out
 
 
@@ -698,8 +699,9 @@ def window_prefill(wp: WindowPlan, q, k_pool, v_pool, block_table, out=None, ws=
     out, ws, ws_ptr, ws_bytes = _step_tensors(wp, q, k_pool, v_pool, block_table, out, ws, stream,
                                               device)
     _call(device, stream, load_library().pa_window_prefill, "pa_window_prefill", wp.ref,
-          *wp.lens_ptrs, wp.window, wp.n_sinks, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(),
-          block_table.shape[1], k_pool.shape[0], out.data_ptr(), ws_ptr, ws_bytes)
+          *wp.lens_ptrs, wp.window, wp.n_sinks, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+          block_table.data_ptr(), block_table.shape[1], k_pool.shape[0], out.data_ptr(), ws_ptr,
+          ws_bytes)
     return out
 
 

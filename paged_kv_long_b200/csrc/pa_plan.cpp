@@ -499,6 +499,16 @@ DecodeWork decode_work(int num_sms, int D, int G, int Hkv, int64_t batch, int64_
   return w;
 }
 
+// The prefix's kernel and the own keys' stream kernel either run one after the other, each on the
+// whole GPU, or side by side: the prefix's grid leaves `aside` SMs free, and the stream kernel,
+// launched as soon as the prefix's CTAs run, takes them. Both start cold (10-12 us), so side by
+// side is most often the shorter: 32 sequences on 32,768 keys, 16 + 2 heads of 256, up to 1,024
+// own keys: 53 us one after the other, 43 / 40 / 38 / 39 / 41 with 24 / 32 / 40 / 48 / 64 SMs
+// aside. It needs the prefix's units in one wave, since the stream kernel starts with its last
+// CTA. The model's times were measured (us): a KV tile of the prefix 1.35 on a CTA pair, 1.95 on
+// one CTA at head dim 256, 1.4 at 128; a tile, or a unit's start, of the stream kernel with two
+// CTAs an SM 2.4 and 1.6, and 6 TB/s over all of it. Own lengths count as half their
+// bound.
 PrefixWork prefix_work(int num_sms, int D, int G, int Hkv, int64_t batch, int64_t prefix_len,
                        int64_t max_len) {
   PrefixWork w;
@@ -506,27 +516,56 @@ PrefixWork prefix_work(int num_sms, int D, int G, int Hkv, int64_t batch, int64_
   w.q_tiles = (int32_t)q_tiles_for(batch, G);
   w.per = D == 256 && w.q_tiles > 1 ? 2 : 1;
   const int64_t tiles = ceil_div64(prefix_len, kTileKeys);
-  const int64_t own_keys = std::max<int64_t>(1, max_len - prefix_len);
-  w.own = decode_work(num_sms, D, G, Hkv, batch,
-                      ceil_div64(own_keys, kTileKeys) + (prefix_len % kTileKeys ? 1 : 0));
+  const int64_t own_tiles = ceil_div64(std::max<int64_t>(1, max_len - prefix_len), kTileKeys) +
+                            (prefix_len % kTileKeys ? 1 : 0);
+  w.own = decode_work(num_sms, D, G, Hkv, batch, own_tiles);
   if (!w.own.stream) {  // always partials (two splits at least), 32 with the prefix's in all
     w.own.splits = std::min(8, std::max(2, w.own.splits));
     w.own.units = batch * Hkv * w.own.splits;
   }
-  // The split count with the shortest waves of units plus the merge's traffic.
   const int64_t units = ceil_div64(w.q_tiles, w.per) * Hkv;
-  const int64_t slots = std::max(1, num_sms / w.per);
-  const int64_t most = std::min<int64_t>(tiles, w.own.stream ? 148 : PA_MAX_SPLITS - w.own.splits);
+  const int64_t most =
+      std::min<int64_t>(tiles, w.own.stream ? 148 : PA_MAX_SPLITS - w.own.splits);
+  const double tile_us = w.per == 2 ? 1.35 : D == 256 ? 1.95 : 1.4, start_us = 12.0;
+  const double merge_us = 2.0 * batch * G * Hkv * (D + 1) * 4.0 * cm.combine_us_per_byte;
+  const double own_half = 0.5 * batch * Hkv * (own_tiles + 1);  // the last ones part filled
+  const double own_work = (0.8 + D / 160.0) * (own_half + batch * Hkv);
+  const double own_read = own_half * kTileKeys * D * 4.0 / 6.0e6;
+  const auto own_us = [&](int64_t ctas) { return 10.0 + std::max(own_work / ctas, own_read); };
+  const auto pre_us = [&](int64_t waves, int64_t tiles_each) {
+    return waves * (tiles_each * tile_us + start_us);
+  };
+  // One after the other: the fewest splits of each unit length that a few waves hold.
   double best = 0.0;
-  w.splits = 1;
-  for (int64_t S = 1; S <= most; ++S) {
-    const double t = (double)ceil_div64(units * S, slots) *
-                         ((double)ceil_div64(tiles, S) * cm.tile_us + cm.unit_us) +
-                     2.0 * S * batch * G * Hkv * (D + 1) * 4.0 * cm.combine_us_per_byte;
-    if (S == 1 || t < best) {
+  w.splits = 0;
+  const int64_t slots = std::max(1, num_sms / w.per), waves0 = ceil_div64(units, slots);
+  for (int64_t waves = waves0; waves < waves0 + 3; ++waves) {
+    const int64_t S0 = std::min(most, waves * slots / units);
+    for (int64_t each = ceil_div64(tiles, S0);; ++each) {
+      const int64_t S = ceil_div64(tiles, each);
+      const double t = pre_us(ceil_div64(units * S, slots), each) + S * merge_us;
+      if (w.splits && t >= best) break;
       best = t;
       w.splits = (int32_t)S;
     }
+  }
+  if (!w.own.stream) return w;
+  best += own_us(w.own.units);
+  // Side by side: up to where the prefix becomes the longer.
+  const int64_t own_most = w.own.units;
+  for (int aside = 4; aside <= num_sms / 2; aside += 4) {
+    const int64_t S0 = std::min<int64_t>(most, (num_sms - aside) / w.per / units);
+    if (S0 < 1) break;
+    const int64_t each = ceil_div64(tiles, S0), S = ceil_div64(tiles, each);
+    const int64_t ctas = std::min<int64_t>(own_most, aside * kDecCtasPerSm);
+    const double pre = pre_us(1, each), own = own_us(ctas);
+    const double t = std::max(pre, own) + S * merge_us;
+    if (t < best) {
+      best = t;
+      w.splits = (int32_t)S;
+      w.own.units = ctas;
+    }
+    if (pre >= own) break;
   }
   return w;
 }

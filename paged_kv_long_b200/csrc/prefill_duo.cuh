@@ -4,8 +4,8 @@
 // With one Q tile a CTA (prefill_kernel) an SM has one softmax warp per scheduler: its exponentials
 // take 128 x 128 / 16 = 1,024 cycles a tile on the special-function unit, and while it waits for
 // them, reads S or stores P the unit idles; measured 2,450 cycles a tile at head dim 128, of
-// which its two products need 1,024. Here two softmax groups (warps 0-3 and 4-7, a thread a row) run on two
-// tiles that share every K/V tile, so one's exponentials fill the other's gaps and the K/V copies
+// which its two products need 1,024. Here two softmax groups (warps 0-3 and 4-7, a thread a row)
+// run on two tiles that share every K/V tile, so one's exponentials fill the other's gaps and the K/V copies
 // are halved. Warps 8 and 9 issue the MMAs of tile A and of tile B, warps 10 and 11 the copies
 // (kv_copy_role, and Q by tensor copy where G divides 128).
 //
@@ -18,8 +18,7 @@
 // Each issuing warp runs PV(j), QK(j+1) of its tile: while one group's softmax works, the other
 // tile's two products do. A thread that issues for both tiles loses ~950 cycles a tile to its
 // commits and waits (4,850 cycles a pair of tiles, 4,000 as it is; see prefill_pair.cuh on issuing
-// threads). P is
-// announced in two halves, so that the first 64 keys' PV overlaps the second half's exponentials.
+// threads). P is announced in two halves, so that the first 64 keys' PV overlaps the second half's exponentials.
 // The two groups take turns: left alone they fall into step whenever both wait for a K/V tile, and
 // then share the special-function unit and the tensor cores by turns of 3,000 and 2,000 cycles.
 // The commit that announces S(j) covers every MMA its thread issued before, PV(j - 1) among them,

@@ -120,7 +120,14 @@ def test_plan_fields_and_workspace():
     p = mk()  # 256 packed rows a head: one CTA pair per head and split, a wave of 74 pairs at most
     assert p.q_tiles == 2 and p.ctas_per_unit == 2 and 1 < 2 * p.splits <= 74
     assert p.policy == 6 and p.hist_len == 33792
-    assert p.units == 32 * 2 * 9 // 2                 # 8 own tiles and a start a unit
+    # the own part: two CTAs on each SM that the prefix's pairs leave, 8 tiles and a start a unit
+    aside = 148 - 2 * 2 * p.splits
+    assert 2 * 4 <= p.units <= min(2 * aside, 32 * 2 * 9 // 2)
+    q = mk(max_seq_len=33000)                         # fewer own keys: fewer SMs aside
+    assert q.splits >= p.splits and q.units <= p.units
+    # the prefix's units do not fit one wave: one part after the other, each on every SM
+    q = mk(batch=1024, n_q_heads=32, n_kv_heads=8, head_dim=128)
+    assert q.units == 296
     assert p.ws_bytes == (p.splits * 512 + 512 + 2 * p.units * 8) * 257 * 4
     p = mk(batch=4)
     assert p.q_tiles == 1 and p.ctas_per_unit == 1
