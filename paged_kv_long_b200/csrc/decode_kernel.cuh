@@ -345,7 +345,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& tm_k, const CUten
 #pragma unroll
         for (int h = 0; h < 8; ++h)
           if (t == h && h < G)
-            a.ws_lse[row0 + h] = ls[h] > 0.f ? m_run[h] + log2f(ls[h]) : -INFINITY;
+            a.ws_lse[row0 + h] = row_lse(m_run[h], ls[h]);
       }
     }
   } else if (warp > kMmaWarp) {

@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
             m = m_run[h];
             l = ls[h];
           }
-        a.ws_lse[row0 + t] = l > 0.f ? m + log2f(l) : -INFINITY;
+        a.ws_lse[row0 + t] = row_lse(m, l);
       }
       // O^T is read: the next segment's first PV waits for a P that comes after this.
       tc_fence_before();
@@ -684,11 +684,9 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
 constexpr int kMergeWarps = kStreamRuns / 32;
 
 template <int D, int OUT, bool PREFIX, int WPR>
-__global__ void __launch_bounds__(kStreamRuns, WPR > 1 ? 4 : 1) merge_stream_kernel(const PrefillArgs a,
-                                                                   int64_t grid_ctas,
-                                                                   const float* pre_o,
-                                                                   const float* pre_lse,
-                                                                   int n_pre) {
+__global__ void __launch_bounds__(kStreamRuns, WPR > 1 ? 4 : 1)
+    merge_stream_kernel(const PrefillArgs a, int64_t grid_ctas, const float* pre_o,
+                        const float* pre_lse, int n_pre) {
   static_assert(WPR == 1 || WPR == kMergeWarps, "a row takes a warp or the block");
   constexpr int NV = D / 128;  // float4 columns a lane holds
   __shared__ int32_t run[kStreamRuns + 1], wsum[kMergeWarps];
@@ -751,9 +749,9 @@ __global__ void __launch_bounds__(kStreamRuns, WPR > 1 ? 4 : 1) merge_stream_ker
     };
     const float lse0 = lse_of(lane);
     float M = lse0;
-    for (int64_t i = 32 + lane; i < mine; i += 32) M = fmaxf(M, lse_of(i));
+    for (int64_t i = 32 + lane; i < mine; i += 32) M = max_nan(M, lse_of(i));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
     float W = 0.f;
     float4 acc[NV];
 #pragma unroll
@@ -800,7 +798,7 @@ __global__ void __launch_bounds__(kStreamRuns, WPR > 1 ? 4 : 1) merge_stream_ker
       if (wid < NV) {  // warp v: the 128 columns from 128 v on
         float Mt = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kMergeWarps; ++w) Mt = fmaxf(Mt, wpart[w][0]);
+        for (int w = 0; w < kMergeWarps; ++w) Mt = max_nan(Mt, wpart[w][0]);
         W = 0.f;
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll

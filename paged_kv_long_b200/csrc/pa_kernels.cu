@@ -439,7 +439,7 @@ __device__ __forceinline__ void write_row(const PrefillArgs& a, const SoftmaxCtx
   if (valid) bulk_store(dst, srow, half ? D * 2 : D * 4);
   bulk_commit();
   bulk_wait_read_all();
-  if (valid && ws_row >= 0) a.ws_lse[ws_row] = l_run > 0.f ? m_run + log2f(l_run) : -INFINITY;
+  if (valid && ws_row >= 0) a.ws_lse[ws_row] = row_lse(m_run, l_run);
 }
 
 __device__ __forceinline__ uint32_t low_bits(int n) {  // bits below n, n clamped to 0 .. 32

@@ -429,6 +429,19 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
   return d;
 }
 
+// The larger of two, NaN if either is (fmaxf drops a NaN).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// Base-2 log-sum-exp of a row with maximum m and sum l of its powers: -inf for a row without a
+// key (l = 0), NaN for one with a NaN among its scores, which its merge has to pass on.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : m + log2f(l);
+}
+
 // 2^x on the special-function unit (PTX ex2.approx.ftz.f32); 2^-inf = +0.
 __device__ __forceinline__ float ex2(float x) {
   float y;

@@ -579,3 +579,44 @@ def test_gpu_window_decode_graph_replay_and_streams():
         step.check(out[live], what=str(new))
         assert all((out[i] == 0).all() for i in range(B) if not new[i])
     del g
+
+
+@_gpu
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 2, 256), (32, 8, 128), (8, 8, 64), (24, 2, 128)])
+@pytest.mark.parametrize("L", [100, 5000])
+def test_gpu_nan_reaches_the_output(Hq, Hkv, D, L):
+    """A query or the keys of a sequence with a NaN, or an infinite query: that head's row is NaN
+    whether its keys are split or not, and no other row changes."""
+    import torch
+    bd = _binding()
+    gen = torch.Generator(device="cuda").manual_seed(L + D)
+    B, PS = 3, 16
+    n = -(-L // PS)
+    k, v = (torch.randn(B * n, PS, Hkv, D, generator=gen, device="cuda").half() for _ in range(2))
+    table = torch.arange(B * n, device="cuda", dtype=torch.int32).view(B, n)
+    lens = torch.full((B,), L, device="cuda", dtype=torch.int32)
+    q = torch.randn(B, Hq, D, generator=gen, device="cuda").half()
+    wd = bd.window_decode_plan(Hq, Hkv, D, PS, B, L, 10**6, 0, "f16")
+    wp = bd.window_plan(Hq, Hkv, D, PS, [1] * B, [L - 1] * B, 10**6, 0, "f16")
+    dp = bd.decode_plan(Hq, Hkv, D, PS, B, L, "f16")
+    common = (L // 2) // PS
+    pd = bd.prefix_decode_plan(Hq, Hkv, D, PS, B, common * PS, L, "f16")
+    shared = table.clone()
+    shared[:, :common] = table[0, :common]
+    runs = {"window decode": lambda q, k: bd.window_decode(wd, q, k, v, table, lens),
+            "window prefill": lambda q, k: bd.window_prefill(wp, q, k, v, table),
+            "decode": lambda q, k: bd.decode(dp, q, k, v, table, lens),
+            "prefix decode": lambda q, k: bd.prefix_decode(pd, q, k, v, table[0, :common].clone(),
+                                                           shared, lens)}
+    bad_q = q.clone()
+    bad_q[1, 0, 3], bad_q[2, 1, 5] = float("nan"), float("inf")
+    bad_k = k.clone()
+    bad_k[n + common:2 * n, :, :, 0] = float("nan")  # sequence 1's keys past the shared pages
+    for name, run in runs.items():
+        want, got, keys = run(q, k), run(bad_q, k), run(q, bad_k)
+        rows = torch.zeros(B, Hq, dtype=torch.bool, device="cuda")
+        rows[1, 0] = rows[2, 1] = True
+        assert bool(got[rows].isnan().all()), name
+        assert torch.equal(got[~rows], want[~rows]), name
+        assert bool(keys[1].isnan().all()), name
+        assert torch.equal(keys[[0, 2]], want[[0, 2]]), name
