@@ -575,6 +575,9 @@ __global__ void __launch_bounds__(kThreads, kDecCtasPerSm)
     stream_copy_role<NP, NSLOT, C::PANEL_LOG>(a, &tm_k, &tm_v, run, x0, slots,
                                               warp - kMmaWarp - 1, sb + C::RING_OFF,
                                               bar(C::B_FULL), bar(C::B_EMPTY), abort_flag, tmo);
+    // All data has landed: the merge starts, and reads the lengths, while the last tiles' products
+    // and epilogues run (2 us a call less than from this grid's end).
+    launch_dependents();
   } else {
     // ============================================================ MMA issuer (one lane)
     if (lane == 0) {
@@ -694,8 +697,9 @@ __global__ void __launch_bounds__(kStreamRuns, WPR > 1 ? 4 : 1)
   __shared__ float4 opart[WPR > 1 ? kMergeWarps : 1][NV][32];         // their weighted rows
   stream_scan(a, run, wsum, false);
   // Launched while the stream kernel ends (programmatic launch): its results are complete past
-  // this wait. The lengths above were there before it.
-  wait_dependencies();
+  // wait_dependencies, which every thread has to pass. The lengths were there before it, so the
+  // first row's place is worked out ahead of the wait.
+  bool waited = false;
   const StreamShare share(run[kStreamRuns], grid_ctas);
   const int lane = threadIdx.x & 31, wid = threadIdx.x / 32;
   const int64_t rows = (int64_t)a.batch * a.Hq;
@@ -723,6 +727,8 @@ __global__ void __launch_bounds__(kStreamRuns, WPR > 1 ? 4 : 1)
       late = share.first(c0) < off;  // the run begins in an earlier unit
     }
     if (!PREFIX && whole) continue;  // the stream kernel wrote the output
+    if (!waited) wait_dependencies();
+    waited = true;
     // Part p: of the prefix (p < n_pre), else of the unit.
     const int64_t unit0 = PREFIX ? rows : 0;  // rows of the workspace before the part slots
     const int64_t total = (PREFIX ? n_pre : 0) + np;
@@ -824,4 +830,5 @@ __global__ void __launch_bounds__(kStreamRuns, WPR > 1 ? 4 : 1)
           make_uint2(pack2<OUT == kOutBf16>(acc[v].x * inv, acc[v].y * inv),
                      pack2<OUT == kOutBf16>(acc[v].z * inv, acc[v].w * inv));
   }
+  if (!waited) wait_dependencies();
 }
