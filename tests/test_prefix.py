@@ -285,3 +285,57 @@ def test_gpu_graph_replay_follows_lengths_and_reports_bad_pages():
     bad[3] = -1
     bd.prefix_decode(pp, q, k.nan_to_num(), v.nan_to_num(), dev(bad), table, lens, out, ws)
     assert bd.device_error(reset=True)[0] == -6
+
+
+@_gpu
+@pytest.mark.parametrize("op", ["prefix", "window"])
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 2, 256), (32, 8, 128), (8, 8, 64)])
+def test_gpu_calls_in_a_row_share_a_workspace(op, Hq, Hkv, D):
+    """The kernels of a call overlap (the own keys run beside the prefix, the merge starts early):
+    calls one after another on one workspace, with the queries and lengths copied in between them
+    in stream order, on two streams at once, give the bits of calls that ran alone."""
+    import torch
+    bd = _binding()
+    PS, B, prefix, most = 16, 12, 4096, 4096 + 900
+    rng = np.random.default_rng(D + Hkv)
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    n = -(-most // PS)
+    table = torch.from_numpy(rng.permutation(B * n).astype(np.int32).reshape(B, n)).cuda()
+    table[:, :prefix // PS] = table[0, :prefix // PS].clone()
+    pre = table[0, :prefix // PS].clone()
+    k, v = (torch.randn(B * n, PS, Hkv, D, generator=gen, device="cuda").half() for _ in range(2))
+    steps = 24
+    qs = torch.randn(steps, B, Hq, D, generator=gen, device="cuda").half()
+    lens = torch.from_numpy(rng.integers(prefix - 3, most, (steps, B)).astype(np.int32)).cuda()
+    if op == "prefix":
+        plan = bd.prefix_decode_plan(Hq, Hkv, D, PS, B, prefix, most, "f16")
+    else:
+        plan = bd.window_decode_plan(Hq, Hkv, D, PS, B, most, 2000, 5, "f16")
+
+    def call(q, length, out, ws, stream=None):
+        if op == "prefix":
+            return bd.prefix_decode(plan, q, k, v, pre, table, length, out, ws, stream)
+        return bd.window_decode(plan, q, k, v, table, length, out, ws, stream)
+
+    alone = []
+    for i in range(steps):
+        alone.append(call(qs[i].clone(), lens[i].clone(), None, bd.workspace(plan.plan)))
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    state = [(torch.empty_like(qs[0]), torch.empty_like(lens[0]), torch.empty_like(qs[0]),
+              bd.workspace(plan.plan)) for _ in streams]
+    keep = [torch.empty(steps, B, Hq, D, dtype=torch.half, device="cuda") for _ in streams]
+    torch.cuda.synchronize()
+    for i in range(steps):
+        for j, s in enumerate(streams):
+            q, length, out, ws = state[j]
+            at = i if j == 0 else steps - 1 - i
+            with torch.cuda.stream(s):
+                q.copy_(qs[at])
+                length.copy_(lens[at])
+                call(q, length, out, ws)
+                keep[j][at].copy_(out)
+    torch.cuda.synchronize()
+    for i in range(steps):
+        assert torch.equal(keep[0][i], alone[i]) and torch.equal(keep[1][i], alone[i]), i
+    assert bd.device_error(reset=True)[0] == 0
