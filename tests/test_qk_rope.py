@@ -184,6 +184,7 @@ def test_refusals():
     assert call(eps=-1.0) == call(eps=float("nan")) == call(eps=float("inf")) == bad
     assert call(D=96) == call(PS=24) == call(rot=8) == call(rot=144) == call(rot=24) == uns
     assert call(pages=1 << 27) == uns
+    assert call(Hq=1 << 30, qs=1 << 38) == call(Hkv=1 << 30, ks=1 << 38, vs=1 << 38) == uns
     assert call(rows=0) == "PA_OK"  # nothing to do
 
 
