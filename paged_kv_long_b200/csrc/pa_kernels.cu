@@ -1487,7 +1487,8 @@ cudaError_t launch_stream(int64_t ctas, cudaStream_t st, const CUtensorMap& tk,
   e = cudaLaunchKernelEx(&main, decode_stream_kernel<D, BF16, !PREFIX>, tk, tv, a);
   if (e != cudaSuccess) return e;
   // A block a row where a row has eight parts or more, and a warp a row where it has a few (most
-  // often none: the stream kernel wrote it).
+  // often none: the stream kernel wrote it). The window decode of 32 sequences, 5 parts a row:
+  // 53.7 us with blocks, 52.2 with warps.
   const int64_t rows = (int64_t)a.batch * a.Hq;
   const bool block_rows = n_pre + ctas / ((int64_t)a.batch * a.Hkv) >= 8;
   const int64_t blocks = block_rows ? rows : ceil_div64(rows, kMergeWarps);

@@ -508,7 +508,9 @@ DecodeWork decode_work(int num_sms, int D, int G, int Hkv, int64_t batch, int64_
 // CTA. The model's times were measured (us): a KV tile of the prefix 1.35 on a CTA pair, 1.95 on
 // one CTA at head dim 256, 1.4 at 128; a tile, or a unit's start, of the stream kernel with two
 // CTAs an SM 2.4 and 1.6, and 6 TB/s over all of it. Own lengths count as half their
-// bound.
+// bound, and side by side the stream kernel as a fifth longer for the HBM it shares (without that
+// 32 sequences of 32 + 8 heads of 128 on 32,768 keys took 57.4 us instead of 52.7, and 64 on 8,192
+// 36.6 instead of 32.6).
 PrefixWork prefix_work(int num_sms, int D, int G, int Hkv, int64_t batch, int64_t prefix_len,
                        int64_t max_len) {
   PrefixWork w;
@@ -558,7 +560,7 @@ PrefixWork prefix_work(int num_sms, int D, int G, int Hkv, int64_t batch, int64_
     if (S0 < 1) break;
     const int64_t each = ceil_div64(tiles, S0), S = ceil_div64(tiles, each);
     const int64_t ctas = std::min<int64_t>(own_most, aside * kDecCtasPerSm);
-    const double pre = pre_us(1, each), own = own_us(ctas);
+    const double pre = pre_us(1, each), own = 1.2 * own_us(ctas);
     const double t = std::max(pre, own) + S * merge_us;
     if (t < best) {
       best = t;
