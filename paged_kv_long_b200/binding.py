@@ -633,12 +633,26 @@ def _call(device: int, stream, fn, name, *args):
         raise PaError(st, name)
 
 
-def _used_on(stream, *tensors):
-    """Tensors made here (on the current stream) that the call uses on `stream`: their memory is
-    not handed out again before that work is done."""
+def _new(stream, make, *args, **kw):
+    """make(*args, **kw): a tensor that this call's kernels write. It comes from the memory of the
+    stream that they run on: a block that the current stream has just freed may still be in use by
+    that stream's pending work, which `stream` does not wait for."""
+    import torch
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
+def _handed_back(stream, device: int, t):
+    """A tensor of _new that the caller gets, most likely to use it on the current stream: once
+    freed, its memory waits for that stream's work too."""
+    import torch
     if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+        current = torch.cuda.current_stream(device)
+        if current != stream:
+            t.record_stream(current)
+    return t
 
 
 def _step_tensors(sp: _StepPlan, q, k_pool, v_pool, block_table, out, ws, stream, device):
@@ -656,15 +670,13 @@ def _step_tensors(sp: _StepPlan, q, k_pool, v_pool, block_table, out, ws, stream
     if block_table.dim() != 2 or block_table.shape[0] != sp.batch:
         raise ValueError("block_table must be [batch, max_pages]")
     if out is None:
-        out = torch.empty_like(q)
-        _used_on(stream, out)
+        out = _handed_back(stream, device, _new(stream, torch.empty_like, q))
     else:
         _require(out, "out", dt, sp.q_shape, device)
     if sp.ws_numel == 0:
         return out, None, None, 0
     if ws is None:
-        ws = torch.empty(sp.ws_numel, dtype=torch.float32, device=q.device)
-        _used_on(stream, ws)
+        ws = _new(stream, torch.empty, sp.ws_numel, dtype=torch.float32, device=q.device)
         return out, ws, ws.data_ptr(), 4 * sp.ws_numel
     _require(ws, "ws", torch.float32, None, device)
     return out, ws, ws.data_ptr(), 4 * ws.numel()
@@ -776,8 +788,8 @@ def block_tables(q_lens, hist_lens, free_pages, pages_used, block_table, max_row
         raise ValueError("block_table must be [batch, max_pages]")
     sizes = (max_rows, max_rows, B + 1, B, 1)
     if out is None:  # one allocation for all five
-        buf = q_lens.new_empty(2 * max_rows + 2 * B + 2)
-        _used_on(stream, buf)
+        buf = _handed_back(stream, device, _new(stream, q_lens.new_empty,
+                                                2 * max_rows + 2 * B + 2))
         # integer parts have no gradient to track as views: this split takes 1 us less
         out = StepTables._make(torch.unsafe_split_with_sizes(buf, sizes))
     else:
@@ -865,8 +877,8 @@ def qk_rope_append(q, k, v, positions, slots, rope, k_pool, v_pool, q_weight=Non
     if k_weight is not None:
         kw = k_weight.data_ptr()
     if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        _used_on(stream, q_out)
+        q_out = _handed_back(stream, device, _new(stream, torch.empty_like, q,
+                                                  memory_format=torch.contiguous_format))
     else:
         _require(q_out, "q_out", dt, (T, Hq, D), device)
     _call(device, stream, load_library().pa_qk_rope_append, "pa_qk_rope_append", Hq, Hkv, D, PS,
