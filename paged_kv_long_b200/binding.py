@@ -206,24 +206,23 @@ def kv_append(k_new, v_new, k_pool, v_pool, page_table, hist_len: int, stream=No
     if k_new.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError("k_new must be float16 or bfloat16")
     dt = k_new.dtype
-    _require_cuda(k_new, "k_new", dt)
+    device = _device_of(k_new, "k_new")
+    _require(k_new, "k_new", dt, None, device)
     if k_new.dim() != 3:
         raise ValueError("k_new must be [R, Hkv, D]")
     R, Hkv, D = k_new.shape
-    _require_cuda(v_new, "v_new", dt, (R, Hkv, D))
-    _require_cuda(k_pool, "k_pool", dt)
+    _require(v_new, "v_new", dt, (R, Hkv, D), device)
+    _require(k_pool, "k_pool", dt, None, device)
     if k_pool.dim() != 4 or tuple(k_pool.shape[2:]) != (Hkv, D):
         raise ValueError("k_pool must be [num_pages, page_size, Hkv, D]")
-    _require_cuda(v_pool, "v_pool", dt, tuple(k_pool.shape))
-    _require_cuda(page_table, "page_table", torch.int32)
+    _require(v_pool, "v_pool", dt, tuple(k_pool.shape), device)
+    _require(page_table, "page_table", torch.int32, None, device)
     PS = k_pool.shape[1]
     if page_table.numel() < math.ceil((hist_len + R) / PS):
         raise ValueError("page_table is shorter than ceil((hist_len+R)/page_size)")
-    st = load_library().pa_kv_append(Hkv, D, PS, _dtype_code(dt), k_new.data_ptr(),
-                                     v_new.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
-                                     page_table.data_ptr(), k_pool.shape[0], hist_len, R,
-                                     _stream_ptr(stream))
-    _check(st, "pa_kv_append")
+    _call(device, stream, load_library().pa_kv_append, "pa_kv_append", Hkv, D, PS,
+          _dtype_code(dt), k_new.data_ptr(), v_new.data_ptr(), k_pool.data_ptr(),
+          v_pool.data_ptr(), page_table.data_ptr(), k_pool.shape[0], hist_len, R)
 
 
 def kv_publish(k_staged, v_staged, k_pool, v_pool, page_table, first_pos: int, rows: int,
@@ -234,26 +233,25 @@ def kv_publish(k_staged, v_staged, k_pool, v_pool, page_table, first_pos: int, r
     if k_staged.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError("k_staged must be float16 or bfloat16")
     dt = k_staged.dtype
-    _require_cuda(k_staged, "k_staged", dt)
+    device = _device_of(k_staged, "k_staged")
+    _require(k_staged, "k_staged", dt, None, device)
     if k_staged.dim() != 3:
         raise ValueError("k_staged must be [T, Hkv, D]")
     T, Hkv, D = k_staged.shape
     if first_pos < 0 or rows < 0 or first_pos + rows > T:
         raise ValueError("rows [first_pos, first_pos + rows) must lie in the staging buffer")
-    _require_cuda(v_staged, "v_staged", dt, (T, Hkv, D))
-    _require_cuda(k_pool, "k_pool", dt)
+    _require(v_staged, "v_staged", dt, (T, Hkv, D), device)
+    _require(k_pool, "k_pool", dt, None, device)
     if k_pool.dim() != 4 or tuple(k_pool.shape[2:]) != (Hkv, D):
         raise ValueError("k_pool must be [num_pages, page_size, Hkv, D]")
-    _require_cuda(v_pool, "v_pool", dt, tuple(k_pool.shape))
-    _require_cuda(page_table, "page_table", torch.int32)
+    _require(v_pool, "v_pool", dt, tuple(k_pool.shape), device)
+    _require(page_table, "page_table", torch.int32, None, device)
     PS = k_pool.shape[1]
     if page_table.numel() < math.ceil((first_pos + rows) / PS):
         raise ValueError("page_table is shorter than ceil((first_pos+rows)/page_size)")
-    st = load_library().pa_kv_publish(Hkv, D, PS, _dtype_code(dt), k_staged.data_ptr(),
-                                      v_staged.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
-                                      page_table.data_ptr(), k_pool.shape[0], first_pos, rows,
-                                      _stream_ptr(stream))
-    _check(st, "pa_kv_publish")
+    _call(device, stream, load_library().pa_kv_publish, "pa_kv_publish", Hkv, D, PS,
+          _dtype_code(dt), k_staged.data_ptr(), v_staged.data_ptr(), k_pool.data_ptr(),
+          v_pool.data_ptr(), page_table.data_ptr(), k_pool.shape[0], first_pos, rows)
 
 
 def _stream_ptr(stream):
@@ -293,13 +291,14 @@ def prefill(p: Plan, q, k_pool, v_pool, page_table, out, ws=None, stream=None):
     import torch
     dt = _torch_dtype(p)
     R, Hq, Hkv, D = p.chunk_rows, p.n_q_heads, p.n_kv_heads, p.head_dim
-    _require_cuda(q, "q", dt, (R, Hq, D))
-    _require_cuda(k_pool, "k_pool", dt)
-    _require_cuda(v_pool, "v_pool", dt, tuple(k_pool.shape))
+    device = _device_of(q, "q")
+    _require(q, "q", dt, (R, Hq, D), device)
+    _require(k_pool, "k_pool", dt, None, device)
+    _require(v_pool, "v_pool", dt, tuple(k_pool.shape), device)
     if p.paged:
         if k_pool.dim() != 4 or tuple(k_pool.shape[1:]) != (p.page_size, Hkv, D):
             raise ValueError("k_pool must be [num_pages, page_size, Hkv, D]")
-        _require_cuda(page_table, "page_table", torch.int32)
+        _require(page_table, "page_table", torch.int32, None, device)
         if page_table.numel() < math.ceil((p.hist_len + R) / p.page_size):
             raise ValueError("page_table is shorter than ceil((H+R)/page_size)")
         num_pages, tab = k_pool.shape[0], page_table.data_ptr()
@@ -309,15 +308,14 @@ def prefill(p: Plan, q, k_pool, v_pool, page_table, out, ws=None, stream=None):
         num_pages, tab = 0, None
     out_ptr, ws_ptr, ws_bytes = None, None, 0
     if p.splits == 1 or p.policy == PA_POLICY_BALANCED:
-        _require_cuda(out, "out", torch.float32, (R, Hq, D))
+        _require(out, "out", torch.float32, (R, Hq, D), device)
         out_ptr = out.data_ptr()
     if p.ws_bytes > 0:
-        _require_cuda(ws, "ws", torch.float32)
+        _require(ws, "ws", torch.float32, None, device)
         ws_ptr, ws_bytes = ws.data_ptr(), ws.numel() * 4
-    st = load_library().pa_prefill(ctypes.byref(p), q.data_ptr(), k_pool.data_ptr(),
-                                   v_pool.data_ptr(), tab, num_pages, p.hist_len, R, out_ptr,
-                                   ws_ptr, ws_bytes, _stream_ptr(stream))
-    _check(st, "pa_prefill")
+    _call(device, stream, load_library().pa_prefill, "pa_prefill", ctypes.byref(p), q.data_ptr(),
+          k_pool.data_ptr(), v_pool.data_ptr(), tab, num_pages, p.hist_len, R, out_ptr, ws_ptr,
+          ws_bytes)
 
 
 def combine(p: Plan, ws, out, stream=None):
@@ -325,21 +323,22 @@ def combine(p: Plan, ws, out, stream=None):
     import torch
     if p.ws_bytes == 0:
         return
-    _require_cuda(ws, "ws", torch.float32)
-    _require_cuda(out, "out", torch.float32, (p.chunk_rows, p.n_q_heads, p.head_dim))
-    st = load_library().pa_combine(ctypes.byref(p), ws.data_ptr(), ws.numel() * 4, out.data_ptr(),
-                                   _stream_ptr(stream))
-    _check(st, "pa_combine")
+    device = _device_of(ws, "ws")
+    _require(ws, "ws", torch.float32, None, device)
+    _require(out, "out", torch.float32, (p.chunk_rows, p.n_q_heads, p.head_dim), device)
+    _call(device, stream, load_library().pa_combine, "pa_combine", ctypes.byref(p),
+          ws.data_ptr(), ws.numel() * 4, out.data_ptr())
 
 
 def prefill_combine(p: Plan, q, k_pool, v_pool, page_table, out=None, ws=None, stream=None):
     """pa_prefill followed by pa_combine; allocates out / ws with torch when not given."""
     import torch
     if out is None:
-        out = torch.empty((p.chunk_rows, p.n_q_heads, p.head_dim), dtype=torch.float32,
-                          device=q.device)
+        out = _handed_back(stream, _device_of(q, "q"),
+                           _new(stream, torch.empty, (p.chunk_rows, p.n_q_heads, p.head_dim),
+                                dtype=torch.float32, device=q.device))
     if p.ws_bytes > 0 and ws is None:
-        ws = workspace(p, q.device)
+        ws = _new(stream, workspace, p, q.device)
     prefill(p, q, k_pool, v_pool, page_table, out, ws, stream)
     combine(p, ws, out, stream)
     return out
@@ -351,19 +350,19 @@ def prefill_noalloc(p: Plan, q, k_pool, v_pool, page_table, out, stream=None):
     import torch
     dt = _torch_dtype(p)
     R, Hq, D = p.chunk_rows, p.n_q_heads, p.head_dim
-    _require_cuda(q, "q", dt, (R, Hq, D))
-    _require_cuda(k_pool, "k_pool", dt)
-    _require_cuda(v_pool, "v_pool", dt, tuple(k_pool.shape))
-    _require_cuda(out, "out", torch.float32, (R, Hq, D))
+    device = _device_of(q, "q")
+    _require(q, "q", dt, (R, Hq, D), device)
+    _require(k_pool, "k_pool", dt, None, device)
+    _require(v_pool, "v_pool", dt, tuple(k_pool.shape), device)
+    _require(out, "out", torch.float32, (R, Hq, D), device)
     if p.paged:
-        _require_cuda(page_table, "page_table", torch.int32)
+        _require(page_table, "page_table", torch.int32, None, device)
         num_pages, tab = k_pool.shape[0], page_table.data_ptr()
     else:
         num_pages, tab = 0, None
-    st = load_library().pa_prefill_noalloc(ctypes.byref(p), q.data_ptr(), k_pool.data_ptr(),
-                                           v_pool.data_ptr(), tab, num_pages, p.hist_len, R,
-                                           out.data_ptr(), _stream_ptr(stream))
-    _check(st, "pa_prefill_noalloc")
+    _call(device, stream, load_library().pa_prefill_noalloc, "pa_prefill_noalloc",
+          ctypes.byref(p), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), tab, num_pages,
+          p.hist_len, R, out.data_ptr())
 
 
 def decode_plan(n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, batch: int,
@@ -388,32 +387,33 @@ def decode(p: Plan, q, k_pool, v_pool, block_table, seq_lens, out=None, ws=None,
     import torch
     dt = _torch_dtype(p)
     B, Hq, Hkv, D, PS = p.batch, p.n_q_heads, p.n_kv_heads, p.head_dim, p.page_size
-    _require_cuda(q, "q", dt, (B, Hq, D))
-    _require_cuda(k_pool, "k_pool", dt)
-    _require_cuda(v_pool, "v_pool", dt, tuple(k_pool.shape))
+    device = _device_of(q, "q")
+    _require(q, "q", dt, (B, Hq, D), device)
+    _require(k_pool, "k_pool", dt, None, device)
+    _require(v_pool, "v_pool", dt, tuple(k_pool.shape), device)
     if k_pool.dim() != 4 or tuple(k_pool.shape[1:]) != (PS, Hkv, D):
         raise ValueError("k_pool must be [num_pages, page_size, Hkv, D]")
-    _require_cuda(block_table, "block_table", torch.int32)
+    _require(block_table, "block_table", torch.int32, None, device)
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [batch, max_pages]")
-    _require_cuda(seq_lens, "seq_lens", torch.int32, (B,))
+    _require(seq_lens, "seq_lens", torch.int32, (B,), device)
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
-    _require_cuda(out, "out", torch.float32, (B, Hq, D))
+        out = _handed_back(stream, device, _new(stream, torch.empty, (B, Hq, D),
+                                                dtype=torch.float32, device=q.device))
+    _require(out, "out", torch.float32, (B, Hq, D), device)
     ws_ptr, ws_bytes = None, 0
     if p.ws_bytes > 0:
         if ws is None:
-            ws = workspace(p, q.device)
-        _require_cuda(ws, "ws", torch.float32)
+            ws = _new(stream, workspace, p, q.device)
+        _require(ws, "ws", torch.float32, None, device)
         ws_ptr, ws_bytes = ws.data_ptr(), ws.numel() * 4
     lib = load_library()
-    st = lib.pa_decode(ctypes.byref(p), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
-                       block_table.data_ptr(), block_table.stride(0), seq_lens.data_ptr(),
-                       k_pool.shape[0], out.data_ptr(), ws_ptr, ws_bytes, _stream_ptr(stream))
-    _check(st, "pa_decode")
+    _call(device, stream, lib.pa_decode, "pa_decode", ctypes.byref(p), q.data_ptr(),
+          k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), block_table.stride(0),
+          seq_lens.data_ptr(), k_pool.shape[0], out.data_ptr(), ws_ptr, ws_bytes)
     if p.ws_bytes > 0:
-        _check(lib.pa_combine(ctypes.byref(p), ws_ptr, ws_bytes, out.data_ptr(),
-                              _stream_ptr(stream)), "pa_combine")
+        _call(device, stream, lib.pa_combine, "pa_combine", ctypes.byref(p), ws_ptr, ws_bytes,
+              out.data_ptr())
     return out
 
 
@@ -473,32 +473,32 @@ def batch_prefill(bp: BatchPlan, q, k_pool, v_pool, block_table, out=None, ws=No
     p = bp.plan
     dt = _torch_dtype(p)
     rows, Hq, Hkv, D, PS = p.chunk_rows, p.n_q_heads, p.n_kv_heads, p.head_dim, p.page_size
-    _require_cuda(q, "q", dt, (rows, Hq, D))
-    _require_cuda(k_pool, "k_pool", dt)
-    _require_cuda(v_pool, "v_pool", dt, tuple(k_pool.shape))
+    device = _device_of(q, "q")
+    _require(q, "q", dt, (rows, Hq, D), device)
+    _require(k_pool, "k_pool", dt, None, device)
+    _require(v_pool, "v_pool", dt, tuple(k_pool.shape), device)
     if k_pool.dim() != 4 or tuple(k_pool.shape[1:]) != (PS, Hkv, D):
         raise ValueError("k_pool must be [num_pages, page_size, Hkv, D]")
-    _require_cuda(block_table, "block_table", torch.int32)
+    _require(block_table, "block_table", torch.int32, None, device)
     if block_table.dim() != 2 or block_table.shape[0] != p.batch:
         raise ValueError("block_table must be [batch, max_pages]")
     if out is None:
-        out = torch.empty((rows, Hq, D), dtype=torch.float32, device=q.device)
-    _require_cuda(out, "out", torch.float32, (rows, Hq, D))
+        out = _handed_back(stream, device, _new(stream, torch.empty, (rows, Hq, D),
+                                                dtype=torch.float32, device=q.device))
+    _require(out, "out", torch.float32, (rows, Hq, D), device)
     ws_ptr, ws_bytes = None, 0
     if p.ws_bytes > 0:
         if ws is None:
-            ws = workspace(p, q.device)
-        _require_cuda(ws, "ws", torch.float32)
+            ws = _new(stream, workspace, p, q.device)
+        _require(ws, "ws", torch.float32, None, device)
         ws_ptr, ws_bytes = ws.data_ptr(), ws.numel() * 4
     ql, hl = bp._arrays()
     lib = load_library()
-    st = lib.pa_batch_prefill(ctypes.byref(p), ql, hl, q.data_ptr(), k_pool.data_ptr(),
-                              v_pool.data_ptr(), block_table.data_ptr(), block_table.stride(0),
-                              k_pool.shape[0], out.data_ptr(), ws_ptr, ws_bytes,
-                              _stream_ptr(stream))
-    _check(st, "pa_batch_prefill")
-    _check(lib.pa_batch_combine(ctypes.byref(p), ql, hl, ws_ptr, ws_bytes, out.data_ptr(),
-                                _stream_ptr(stream)), "pa_batch_combine")
+    _call(device, stream, lib.pa_batch_prefill, "pa_batch_prefill", ctypes.byref(p), ql, hl,
+          q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(),
+          block_table.stride(0), k_pool.shape[0], out.data_ptr(), ws_ptr, ws_bytes)
+    _call(device, stream, lib.pa_batch_combine, "pa_batch_combine", ctypes.byref(p), ql, hl, ws_ptr,
+          ws_bytes, out.data_ptr())
     return out
 
 

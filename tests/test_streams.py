@@ -1,5 +1,6 @@
-"""Calls given a stream that is not the current one: the tensors that a call makes itself come from
-the memory of the stream that its kernels run on.
+"""Calls given a stream that is not the current one, or tensors of a device that is not: a call runs
+on its tensors' device, and the tensors that it makes itself come from the memory of the stream
+that its kernels run on.
 
 A block that the current stream has freed may be handed out again to work of that stream at once,
 because it runs behind the block's last use. Kernels on another stream do not: written there, the
@@ -152,6 +153,93 @@ def test_tensors_made_by_a_call_are_the_calls_streams(fake_device, name):
     assert allocated == [s] * n
     # what the caller gets back is kept for the current stream's work as well; the workspace is not
     assert [x for what, x in made if what == "recorded"] == ["the current one"]
+
+
+def _older_calls(bd, on):
+    """name -> (a call of the entry points without a window or prefix, tensors that it makes)."""
+    import torch
+    f16, f32, i32 = torch.float16, torch.float32, torch.int32
+    pool, table = on(9, 16, 2, 128, dtype=f16), on(9, dtype=i32)
+    q, rows = on(3, 8, 128, dtype=f16), on(3, 2, 128, dtype=f16)
+    tables, lens = on(3, 4, dtype=i32), on(3, dtype=i32)
+    out, ws = on(3, 8, 128, dtype=f32), on(64, dtype=f32)
+    p = _plan_on_host(bd, 0)
+    p.paged, p.splits, p.hist_len = 1, 2, 60
+    bp = bd.BatchPlan(p, [1, 1, 1], [9, 9, 9])
+    return {
+        "append": (lambda s: bd.kv_append(rows, rows, pool, pool, table, 60, s), 0),
+        "publish": (lambda s: bd.kv_publish(rows, rows, pool, pool, table, 0, 3, s), 0),
+        "prefill": (lambda s: bd.prefill(p, q, pool, pool, table, out, ws, s), 0),
+        "combine": (lambda s: bd.combine(p, ws, out, s), 0),
+        "both": (lambda s: bd.prefill_combine(p, q, pool, pool, table, stream=s), 2),
+        "noalloc": (lambda s: bd.prefill_noalloc(p, q, pool, pool, table, out, s), 0),
+        "decode": (lambda s: bd.decode(p, q, pool, pool, tables, lens, stream=s), 2),
+        "batch": (lambda s: bd.batch_prefill(bp, q, pool, pool, tables, stream=s), 2),
+    }
+
+
+OLDER = ("append", "publish", "prefill", "combine", "both", "noalloc", "decode", "batch")
+
+
+@pytest.mark.parametrize("name", OLDER)
+def test_older_calls_too(fake_device, name):
+    calls, made, on = fake_device
+    call, n = _older_calls(_binding(), on)[name]
+    del made[:]
+    s = FakeStream(ctypes.c_void_p(11))
+    call(s)
+    assert calls and [x for _, x in calls] == [s.cuda_stream] * len(calls)
+    assert [x for what, x in made if what != "recorded"] == [s] * n
+    assert [x for what, x in made if what == "recorded"] == ["the current one"] * (n > 0)
+
+
+@pytest.mark.parametrize("name", OLDER + tuple(CALLS))
+def test_calls_run_on_the_device_of_their_tensors(fake_device, monkeypatch, name):
+    """Device 1 is current, the tensors are on device 0."""
+    import torch
+    calls, _, on = fake_device
+    bd = _binding()
+    entered = []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            entered.append((self.index, len(calls)))
+
+        def __exit__(self, *exc):
+            entered.append((None, len(calls)))
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 70 + d)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    if name in CALLS:
+        CALLS[name][0](bd, on, None)
+    else:
+        _older_calls(bd, on)[name][0](None)
+    assert calls and [x for _, x in calls] == [70] * len(calls)
+    # each launch stands between entering device 0 and leaving it
+    assert entered == [e for i in range(len(calls)) for e in ((0, i), (None, i + 1))]
+
+
+@pytest.mark.parametrize("name", ["prefill", "decode", "batch"])
+def test_tensors_of_two_devices_are_refused(fake_device, name):
+    import torch
+    _, _, on = fake_device
+    bd = _binding()
+    far = on(9, 16, 2, 128, dtype=torch.float16)
+    far.get_device = lambda: 1
+    near, p = on(9, 16, 2, 128, dtype=torch.float16), _plan_on_host(bd, 0)
+    p.paged, p.splits = 1, 2
+    q, i32 = on(3, 8, 128, dtype=torch.float16), torch.int32
+    with pytest.raises(ValueError, match="one device"):
+        if name == "prefill":
+            bd.prefill(p, q, far, near, on(9, dtype=i32), None)
+        elif name == "decode":
+            bd.decode(p, q, near, far, on(3, 4, dtype=i32), on(3, dtype=i32))
+        else:
+            bd.batch_prefill(bd.BatchPlan(p, [1] * 3, [9] * 3), q, near, far, on(3, 4, dtype=i32))
 
 
 # ------------------------------------------------------------------------------------ GPU
