@@ -489,7 +489,7 @@ int pa_block_tables(int batch, const int32_t* q_lens, const int32_t* hist_lens, 
  *   k_pool, v_pool device [num_pages][PS][Hkv][D] of dtype; only the rows' slots change.
  * All arithmetic is fp32 (sums of squares too), rounded once to dtype.
  * Returns PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED (head_dim not 64/128/256, rot_dim,
- * page_size, more than 2^20 heads, pools of 2^31 slots) or PA_ERR_CUDA.
+ * page_size, more than 65,535 query or 32,767 key heads, pools of 2^31 slots) or PA_ERR_CUDA.
  */
 int pa_qk_rope_append(int n_q_heads, int n_kv_heads, int head_dim, int page_size, int dtype,
                       int rows, const void* q, int64_t q_stride, const void* k, int64_t k_stride,

@@ -2267,7 +2267,9 @@ extern "C" int pa_qk_rope_append(int n_q_heads, int n_kv_heads, int head_dim, in
     return PA_ERR_INVALID_ARG;
   if (!(eps >= 0.0f) || isinf(eps)) return PA_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return PA_ERR_UNSUPPORTED;
-  if (n_q_heads > (1 << 20) || n_kv_heads > (1 << 20)) return PA_ERR_UNSUPPORTED;  // 32-bit sets
+  // a warp's share of its token's sets is worked out in 32 bits: (its number + 1) * sets, both at
+  // most the heads of one side (queries, or keys and values)
+  if (n_q_heads > 0xffff || n_kv_heads > 0x7fff) return PA_ERR_UNSUPPORTED;
   if (page_size < 16 || page_size > 128 || (page_size & (page_size - 1))) return PA_ERR_UNSUPPORTED;
   if (rot_dim < 16 || rot_dim > head_dim || rot_dim % 16) return PA_ERR_UNSUPPORTED;
   if (num_pages >= ((int64_t(1) << 31) - kTileKeys) / page_size) return PA_ERR_UNSUPPORTED;

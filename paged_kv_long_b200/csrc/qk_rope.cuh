@@ -80,7 +80,8 @@ __global__ void __launch_bounds__(32, 32) qk_rope_append_kernel(const RopeArgs a
     e = turned ? 4 * l : half + 4 * l;             // past rot: rot + (4 l - half)
     f = turned ? half + 4 * l : D / 2 + 4 * l;     // that plus (D - rot) / 2
   }
-  // this warp's share of its token's query sets, or key and value sets
+  // this warp's share of its token's query sets, or key and value sets (32 bits: the host keeps
+  // parts <= sets < 2^16)
   const int n_heads = is_q ? a.Hq : 2 * a.Hkv;
   const uint32_t sets = (n_heads + HPW - 1) / HPW;
   const uint32_t part = is_q ? w : w - a.q_warps, parts = is_q ? a.q_warps : a.kv_warps;

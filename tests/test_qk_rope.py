@@ -188,6 +188,33 @@ def test_refusals():
     assert call(rows=0) == "PA_OK"  # nothing to do
 
 
+MOST_Q, MOST_KV = 65535, 32767
+
+
+def test_most_heads():
+    """One past the heads whose sets a warp's 32-bit shares hold is refused, and the shares of the
+    accepted most cover every set once (the kernel's own arithmetic, in 32 bits)."""
+    lib, bd = _binding().load_library(), _binding()
+    p = ctypes.c_void_p(1 << 20)
+
+    def call(Hq, Hkv, D):
+        return bd.STATUS[lib.pa_qk_rope_append(Hq, Hkv, D, 16, 0, 0, p, Hq * D, p, Hkv * D, p,
+                                               Hkv * D, p, p, p, 64, 100, 0, None, None, 0, 1e-6,
+                                               p, p, p, 8, None)]
+
+    for D in (64, 128, 256):
+        assert call(MOST_Q, 1, D) == call(1, MOST_KV, D) == "PA_OK"
+        assert call(MOST_Q + 1, 1, D) == call(1, MOST_KV + 1, D) == "PA_ERR_UNSUPPORTED"
+        hpw = 256 // D
+        for heads in (MOST_Q, 2 * MOST_KV):
+            sets = -(-heads // hpw)
+            for n in (1, 13, 221, sets):
+                parts = -(-sets // n)
+                part = np.arange(parts + 1, dtype=np.uint32)
+                edge = part * np.uint32(sets) // np.uint32(parts)  # wraps as the kernel's would
+                assert edge[0] == 0 and edge[-1] == sets and (np.diff(edge.astype(int)) > 0).all()
+
+
 def test_binding_refuses_cpu_tensors_and_types():
     import torch
     z = torch.zeros(2, 2, 64, dtype=torch.float16)
@@ -221,6 +248,13 @@ CASES = [
 def test_gpu_qk_rope(case):
     *shape, inter = case
     run_and_check(make(sum(case[:5]), *shape), inter)
+
+
+@_gpu
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(1, MOST_Q, 1, 256), (1, 1, MOST_KV, 64),
+                                        (2, MOST_Q, 3, 64)])
+def test_gpu_most_heads(T, Hq, Hkv, D):
+    run_and_check(make(7, T, Hq, Hkv, D, 32, 16, "f16", max_pos=64))
 
 
 @_gpu
