@@ -360,7 +360,7 @@ int pa_window_decode(const pa_plan_t* plan, int window, int n_sinks, const void*
  *   seq_lens      device int32 [batch]: keys of each whole sequence. A sequence of at most
  *                 prefix_len keys sees its first seq_lens[b] shared ones; one with no key (a
  *                 padded row) gets zeros.
- *   out           device [batch][Hq][D] of dtype.
+ *   out           device [batch][Hq][D] of dtype; it may not overlap q.
  *   lse_ws        workspace of plan->ws_bytes. The call merges its partials itself.
  * The plan's policy is PA_POLICY_PREFIX_DECODE, splits the prefix's splits, units those of the own
  * part; other entry points refuse it, and a prefix_len that needs another launch or workspace than

@@ -1540,6 +1540,12 @@ cudaError_t launch_paged_single(int D, bool bf16, bool sq, int64_t grid, cudaStr
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// The na bytes at a and the nb bytes at b share one.
+bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na > 0 && nb > 0 && (x <= y ? y - x < na : x - y < nb);
+}
+
 }  // namespace pa
 
 using namespace pa;
@@ -1666,11 +1672,12 @@ extern "C" int pa_prefill(const pa_plan_t* plan, const void* q, const void* k_po
 
 namespace pa {
 // Checks of the arguments that every decode entry point takes, its tensor maps (pages of K, V boxes
-// over all of D) and its kernel arguments but for the workspace.
+// over all of D) and its kernel arguments but for the workspace. out16: the output has the type of q
+// and may not overlap it (rows leave while other CTAs still read theirs).
 static int decode_args(const pa_plan_t* plan, const void* q, const void* k_pool,
                        const void* v_pool, const int32_t* block_table, int table_stride,
-                       const int32_t* seq_lens, int64_t num_pages, void* out, CUtensorMap* tk,
-                       CUtensorMap* tv, PrefillArgs* args) {
+                       const int32_t* seq_lens, int64_t num_pages, void* out, bool out16,
+                       CUtensorMap* tk, CUtensorMap* tv, PrefillArgs* args) {
   if (!q || !k_pool || !v_pool || !block_table || !seq_lens || !out || table_stride <= 0 ||
       num_pages <= 0)
     return PA_ERR_INVALID_ARG;
@@ -1681,6 +1688,8 @@ static int decode_args(const pa_plan_t* plan, const void* q, const void* k_pool,
   if (plan->n_q_heads != plan->n_kv_heads * plan->group || plan->group > kTileRows)
     return PA_ERR_INVALID_ARG;
   if (num_pages * PS + kTileKeys >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
+  const uint64_t q_bytes = (uint64_t)B * plan->n_q_heads * D * 2;
+  if (out16 && overlap(q, q_bytes, out, q_bytes)) return PA_ERR_INVALID_ARG;
   const bool bf16 = plan->dtype == PA_BF16;
   const int64_t rows = num_pages * PS;
   const int v_rows = std::min(PS, 128 / (D / 64));
@@ -1733,7 +1742,7 @@ extern "C" int pa_decode(const pa_plan_t* plan, const void* q, const void* k_poo
   CUtensorMap tk, tv;
   PrefillArgs a;
   const int st = decode_args(plan, q, k_pool, v_pool, block_table, table_stride, seq_lens,
-                             num_pages, out, &tk, &tv, &a);
+                             num_pages, out, false, &tk, &tv, &a);
   if (st != PA_OK) return st;
   const bool bf16 = plan->dtype == PA_BF16;
   a.splits = S;
@@ -1782,7 +1791,7 @@ extern "C" int pa_window_decode(const pa_plan_t* plan, int window, int n_sinks, 
   CUtensorMap tk, tv;
   PrefillArgs a;
   const int st = decode_args(plan, q, k_pool, v_pool, block_table, table_stride, seq_lens,
-                             num_pages, out, &tk, &tv, &a);
+                             num_pages, out, true, &tk, &tv, &a);
   if (st != PA_OK) return st;
   const bool bf16 = plan->dtype == PA_BF16;
   if (!stream_args(a, window, n_sinks, 0)) return PA_ERR_UNSUPPORTED;
@@ -1823,7 +1832,7 @@ extern "C" int pa_prefix_decode(const pa_plan_t* plan, int64_t prefix_len, const
   CUtensorMap tk, tv;
   PrefillArgs a;
   int st = decode_args(plan, q, k_pool, v_pool, block_table, table_stride, seq_lens, num_pages,
-                       out, &tk, &tv, &a);
+                       out, true, &tk, &tv, &a);
   if (st != PA_OK) return st;
   const bool bf16 = plan->dtype == PA_BF16;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
@@ -1975,6 +1984,8 @@ static int run_batch(const pa_plan_t* plan, const Window* win, const Batch& bt,
     return PA_ERR_WORKSPACE;
   const int D = plan->head_dim, PS = plan->page_size, per = plan->ctas_per_unit;
   if (num_pages * PS + kTileKeys >= (int64_t(1) << 31)) return PA_ERR_UNSUPPORTED;
+  const uint64_t q_bytes = (uint64_t)bt.total_rows * plan->n_q_heads * D * 2;
+  if (win && overlap(q, q_bytes, out, q_bytes)) return PA_ERR_INVALID_ARG;  // as decode_args
   const bool bf16 = plan->dtype == PA_BF16;
   const int64_t rows = num_pages * PS;
   const bool pair = per == 2 && D == 256;  // else two Q tiles a unit are one CTA's (windows)

@@ -341,6 +341,29 @@ def test_refusals():
     assert prefill(wp) == bad
 
 
+def test_an_output_over_the_queries_is_refused():
+    """Whole or in part, by the window and the prefix calls; an output right behind the queries
+    gets past that check (to the tensor maps, which need a GPU's driver here)."""
+    bd = _binding()
+    lib, ref = bd.load_library(), ctypes.byref
+    q, f, big = 1 << 30, ctypes.c_void_p(1 << 20), 1 << 40
+    wd = bd.window_decode_plan(16, 2, 256, 16, 4, 1000, 200, 4, "f16", num_sms=148)
+    wp = bd.window_plan(16, 2, 256, 16, [1, 3], [50, 60], 200, 4, "f16", num_sms=148)
+    pp = bd.prefix_decode_plan(16, 2, 256, 16, 4, 320, 1000, "f16", num_sms=148)
+    n = 4 * 16 * 256 * 2  # bytes of q, and of the output
+    runs = (lambda out: lib.pa_window_decode(ref(wd.plan), 200, 4, q, f, f, f, 64, f, 100, out, f,
+                                             big, None),
+            lambda out: lib.pa_window_prefill(ref(wp.plan), *wp.lens_ptrs, 200, 4, q, f, f, f, 64,
+                                              100, out, f, big, None),
+            lambda out: lib.pa_prefix_decode(ref(pp.plan), 320, q, f, f, f, f, 64, f, 100, out, f,
+                                             big, None))
+    for run in runs:
+        for out in (q, q + 16, q - 16, q + n - 16, q - n + 16):
+            assert bd.STATUS[run(out)] == "PA_ERR_INVALID_ARG"
+        if not cuda_available():
+            assert bd.STATUS[run(q + n)] == bd.STATUS[run(q - n)] == "PA_ERR_CUDA"
+
+
 def test_plan_keeps_its_own_lengths():
     bd = _binding()
     rows, hist = np.array([3, 5], np.int32), np.array([9, 0], np.int64)
