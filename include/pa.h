@@ -443,8 +443,8 @@ int pa_kv_publish(int n_kv_heads, int head_dim, int page_size, int dtype, const 
  *   free_pages         device int32 [n_free]: pages in no table row; taken in order.
  *   pages_used         device int32 [1]: entries of free_pages that earlier steps took;
  *   pages_used_out     device int32 [1], not the same word: that plus the pages taken here.
- *                      (No output may overlap an input: nothing is updated in place but
- *                      block_table.)
+ *                      (No output may overlap an input or another output: nothing is updated
+ *                      in place but block_table.)
  *   block_table        device int32 [batch][table_stride], updated in place: request b owns
  *                      entries 0 .. ceil(h/PS)-1 (only read) and gets the entries up to
  *                      ceil((h+r)/PS)-1 from the free list, request by request. Others stay.

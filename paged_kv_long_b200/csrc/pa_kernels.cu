@@ -2227,13 +2227,29 @@ extern "C" int pa_block_tables(int batch, const int32_t* q_lens, const int32_t* 
   if (!q_lens || !hist_lens || !pages_used || !pages_used_out || !block_table || !cu_q_lens ||
       !seq_lens || (n_free > 0 && !free_pages) || (max_rows > 0 && (!slots || !positions)))
     return PA_ERR_INVALID_ARG;
-  // every block reads the inputs while the first ones already write: nothing in place
-  for (const int32_t* out : {pages_used_out, block_table, slots, positions, cu_q_lens, seq_lens})
-    if (out && (out == q_lens || out == hist_lens || out == free_pages || out == pages_used))
-      return PA_ERR_INVALID_ARG;
   if (page_size < 16 || page_size > 128 || (page_size & (page_size - 1))) return PA_ERR_UNSUPPORTED;
   if (batch > kStepMaxSeqs || num_pages >= ((int64_t(1) << 31) - kTileKeys) / page_size)
     return PA_ERR_UNSUPPORTED;
+  // Every block reads the inputs while the first ones already write: nothing in place, and the
+  // outputs apart from one another.
+  const struct {
+    const int32_t* at;
+    uint64_t words;
+  } part[] = {{pages_used_out, 1},
+              {block_table, (uint64_t)batch * table_stride},
+              {slots, (uint64_t)max_rows},
+              {positions, (uint64_t)max_rows},
+              {cu_q_lens, (uint64_t)batch + 1},
+              {seq_lens, (uint64_t)batch},
+              {q_lens, (uint64_t)batch},  // the inputs, from here on
+              {hist_lens, (uint64_t)batch},
+              {free_pages, (uint64_t)n_free},
+              {pages_used, 1}};
+  constexpr int n_out = 6, n_all = sizeof part / sizeof part[0];
+  for (int i = 0; i < n_out; ++i)
+    for (int j = i + 1; j < n_all; ++j)
+      if (overlap(part[i].at, 4 * part[i].words, part[j].at, 4 * part[j].words))
+        return PA_ERR_INVALID_ARG;
   // Four rows a thread up to a block per SM: every block repeats the scan of the lengths.
   const int64_t want = ((int64_t)max_rows + 4 * kStepThreads - 1) / (4 * kStepThreads);
   const unsigned blocks = (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, 148));

@@ -152,6 +152,33 @@ def test_refusals():
     assert call(pages=1 << 27) == "PA_ERR_UNSUPPORTED"  # 2^31 slots
 
 
+def test_outputs_that_meet_inputs_or_one_another_are_refused():
+    """Not only at equal pointers: an output that begins inside an input, or ends in one."""
+    lib, bd = _binding().load_library(), _binding()
+    B, F, stride, rows = 3, 9, 4, 8
+    words = dict(q_lens=B, hist_lens=B, free=F, used=1, used_out=1, table=B * stride, slots=rows,
+                 pos=rows, cu=B + 1, seq=B)
+    apart = {name: (1 + i) << 20 for i, name in enumerate(words)}
+
+    def call(**move):
+        a = {**apart, **move}
+        return bd.STATUS[lib.pa_block_tables(B, a["q_lens"], a["hist_lens"], 16, 10, a["free"], F,
+                                             a["used"], a["used_out"], a["table"], stride, rows,
+                                             a["slots"], a["pos"], a["cu"], a["seq"], None)]
+
+    outs = ("used_out", "table", "slots", "pos", "cu", "seq")
+    for out in outs:
+        for other in words:
+            if other != out:
+                last = apart[other] + 4 * (words[other] - 1)  # its last word
+                assert call(**{out: apart[other]}) == "PA_ERR_INVALID_ARG", (out, other)
+                assert call(**{out: last}) == "PA_ERR_INVALID_ARG", (out, other)
+                before = apart[other] - 4 * (words[out] - 1)  # the output's last word on its first
+                assert call(**{out: before}) == "PA_ERR_INVALID_ARG", (out, other)
+                if not cuda_available():  # side by side: past the checks (no device here)
+                    assert call(**{out: last + 4}) == "PA_ERR_CUDA", (out, other)
+
+
 def test_binding_refuses_cpu_tensors():
     import torch
     z = torch.zeros(2, dtype=torch.int32)
