@@ -485,7 +485,7 @@ int pa_block_tables(int batch, const int32_t* q_lens, const int32_t* hist_lens, 
  *                  raises PA_ERR_PAGE_INDEX in pa_device_error. Slots of a call must differ:
  *                  rows of the same slot would leave a mixture of their heads there.
  *   q_out          device [rows][Hq][D] of dtype, contiguous; q itself (q_stride = Hq*D) or memory
- *                  that overlaps no input.
+ *                  that overlaps no input, the gaps between the rows of q, k and v included.
  *   k_pool, v_pool device [num_pages][PS][Hkv][D] of dtype; only the rows' slots change.
  * All arithmetic is fp32 (sums of squares too), rounded once to dtype.
  * Returns PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED (head_dim not 64/128/256, rot_dim,

@@ -2311,6 +2311,13 @@ extern "C" int pa_qk_rope_append(int n_q_heads, int n_kv_heads, int head_dim, in
   for (const void* p : {q, k, v, (const void*)rope, (const void*)q_out, (const void*)k_pool,
                         (const void*)v_pool, q_weight, k_weight})
     if (!aligned16(p)) return PA_ERR_INVALID_ARG;
+  // q_out is q itself (each warp reads its heads before it writes them) or apart from all inputs
+  const uint64_t out_bytes = 2ull * rows * qw;
+  const auto span = [&](int64_t stride, int64_t w) { return 2ull * ((rows - 1) * stride + w); };
+  if ((q != q_out && overlap(q_out, out_bytes, q, span(q_stride, qw))) ||
+      overlap(q_out, out_bytes, k, span(k_stride, kw)) ||
+      overlap(q_out, out_bytes, v, span(v_stride, kw)))
+    return PA_ERR_INVALID_ARG;
   RopeArgs a;
   memset(&a, 0, sizeof a);
   a.q = static_cast<const uint16_t*>(q);

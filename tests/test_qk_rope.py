@@ -215,6 +215,33 @@ def test_most_heads():
                 assert edge[0] == 0 and edge[-1] == sets and (np.diff(edge.astype(int)) > 0).all()
 
 
+def test_rotated_queries_over_an_input_are_refused():
+    """q_out may be q; inside q, or in k or v, it may not be (one fused row holds all three)."""
+    lib, bd = _binding().load_library(), _binding()
+    Hq, Hkv, D, T = 8, 2, 64, 5
+    row = (Hq + 2 * Hkv) * D  # elements of a fused row
+    f, base = ctypes.c_void_p(1 << 20), 1 << 30
+
+    def call(out, q=base, k=base + 2 * Hq * D, v=base + 2 * (Hq + Hkv) * D, stride=row):
+        return bd.STATUS[lib.pa_qk_rope_append(Hq, Hkv, D, 16, 0, T, q, stride, k, stride, v,
+                                               stride, f, f, f, 64, 100, 0, None, None, 0, 1e-6,
+                                               out, f, f, 8, None)]
+
+    bad, nbytes = "PA_ERR_INVALID_ARG", 2 * T * Hq * D
+    end = base + 2 * T * row
+    for out in (base, base + 16, base + 2 * Hq * D, end - 16, base - nbytes + 16):
+        assert call(out) == bad, out - base
+    apart = dict(q=base, k=base + (1 << 24), v=base + (2 << 24), stride=Hq * D)
+    last = 2 * ((T - 1) * Hq * D + Hkv * D)  # bytes that k's (and v's) rows span
+    for out in (base + 16, base - 16, apart["k"], apart["k"] + last - 16, apart["v"] - nbytes + 16):
+        assert call(out, **apart) == bad
+    if not cuda_available():  # past the checks (no device here)
+        ok = "PA_ERR_CUDA"
+        assert call(end) == call(base - nbytes) == ok
+        assert call(base, **apart) == call(base + nbytes, **apart) == ok
+        assert call(apart["k"] + last, **apart) == call(apart["v"] - nbytes, **apart) == ok
+
+
 def test_binding_refuses_cpu_tensors_and_types():
     import torch
     z = torch.zeros(2, 2, 64, dtype=torch.float16)
