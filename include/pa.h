@@ -365,6 +365,8 @@ int pa_window_decode(const pa_plan_t* plan, int window, int n_sinks, const void*
  * The plan's policy is PA_POLICY_PREFIX_DECODE, splits the prefix's splits, units those of the own
  * part; other entry points refuse it, and a prefix_len that needs another launch or workspace than
  * the one it was made with is refused.
+ * PA_ERR_UNSUPPORTED: batch * Hkv * (the most KV tiles a table row reaches past the prefix, plus two)
+ * or batch * Hq passes 2^31.
  */
 int pa_prefix_decode_plan(int num_sms, int n_q_heads, int n_kv_heads, int head_dim, int page_size,
                           int batch, int64_t prefix_len, int64_t max_seq_len, int dtype,

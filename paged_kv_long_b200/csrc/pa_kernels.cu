@@ -1444,28 +1444,35 @@ cudaError_t launch_decode_d(int D, bool bf16, int64_t grid, cudaStream_t st,
                           : launch_decode<256, false, BAL, WIN>(grid, st, tk, tv, a, it));
 }
 
+// The stream kernel's 32-bit view of a table row's keys, a window or a first key.
+constexpr int64_t kStreamMost = (int64_t(1) << 31) - 1 - 2 * kTileKeys;
+
+// Its slots (a unit's KV tiles and its start) and output rows stay below 2^31.
+bool stream_fits(int64_t batch, int64_t Hq, int64_t Hkv, int64_t table_stride, int page_rows,
+                 int64_t window, int64_t sinks, int64_t first_key) {
+  const int64_t cap = std::min(table_stride * page_rows, kStreamMost);
+  const int64_t tiles = std::max<int64_t>(
+      1, std::min(window_most_tiles(cap, window, sinks),
+                  ceil_div64(std::max<int64_t>(cap - first_key, 0), kTileKeys) + 1 +
+                      ceil_div64(sinks, kTileKeys)));
+  return (double)batch * Hkv * (double)(tiles + 1) < 2147483648.0 &&
+         (double)batch * Hq < 2147483648.0;
+}
+
+void stream_args(PrefillArgs& a, int64_t window, int64_t sinks, int64_t first_key) {
+  a.window = window;
+  a.sinks = sinks;
+  a.first_key = first_key;
+  a.seq_cap = (int32_t)std::min((int64_t)a.table_stride * a.page_rows, kStreamMost);
+  a.window32 = (int32_t)std::min(window, kStreamMost);
+  a.sinks32 = (int32_t)std::min(sinks, kStreamMost);
+  a.first_key32 = (int32_t)std::min(first_key, kStreamMost);
+}
+
 // The stream kernel on `ctas` CTAs, then its merge (programmatic launch: the merge's launch
 // overlaps the stream kernel's end). a.ws_o / ws_lse: the rows of the stream kernel's partials.
 // PREFIX: every unit leaves a partial, and n_pre partials of the prefix join (see the kernels);
 // the stream kernel's launch overlaps the prefix's kernel before it.
-// The stream kernel's 32-bit view of a window or a first key. False when its slots could pass 2^31.
-bool stream_args(PrefillArgs& a, int64_t window, int64_t sinks, int64_t first_key) {
-  const int64_t most = (int64_t(1) << 31) - 1 - 2 * kTileKeys;
-  a.window = window;
-  a.sinks = sinks;
-  a.first_key = first_key;
-  a.seq_cap = (int32_t)std::min((int64_t)a.table_stride * a.page_rows, most);
-  a.window32 = (int32_t)std::min(window, most);
-  a.sinks32 = (int32_t)std::min(sinks, most);
-  a.first_key32 = (int32_t)std::min(first_key, most);
-  const int64_t tiles = std::max<int64_t>(
-      1, std::min(window_most_tiles(a.seq_cap, window, sinks),
-                  ceil_div64(std::max<int64_t>(a.seq_cap - first_key, 0), kTileKeys) + 1 +
-                      ceil_div64(sinks, kTileKeys)));
-  return (double)a.batch * a.Hkv * (double)(tiles + 1) < 2147483648.0 &&
-         (double)a.batch * a.Hq < 2147483648.0;
-}
-
 template <int D, bool BF16, bool PREFIX>
 cudaError_t launch_stream(int64_t ctas, cudaStream_t st, const CUtensorMap& tk,
                           const CUtensorMap& tv, const PrefillArgs& a, const float* pre_o,
@@ -1788,13 +1795,16 @@ extern "C" int pa_window_decode(const pa_plan_t* plan, int window, int n_sinks, 
     return PA_ERR_INVALID_ARG;  // not this window's plan
   if (plan->ws_bytes > 0 && (!lse_ws || !aligned16(lse_ws) || ws_bytes < plan->ws_bytes))
     return PA_ERR_WORKSPACE;
+  if (!stream_fits(plan->batch, plan->n_q_heads, plan->n_kv_heads, table_stride, plan->page_size,
+                   window, n_sinks, 0))
+    return PA_ERR_UNSUPPORTED;
   CUtensorMap tk, tv;
   PrefillArgs a;
   const int st = decode_args(plan, q, k_pool, v_pool, block_table, table_stride, seq_lens,
                              num_pages, out, true, &tk, &tv, &a);
   if (st != PA_OK) return st;
   const bool bf16 = plan->dtype == PA_BF16;
-  if (!stream_args(a, window, n_sinks, 0)) return PA_ERR_UNSUPPORTED;
+  stream_args(a, window, n_sinks, 0);
   a.splits = w.splits;
   a.ws_o = plan->ws_bytes > 0 ? lse_ws : nullptr;
   a.ws_lse = plan->ws_bytes > 0 ? lse_ws + w.ws_rows(G, rows) * D : nullptr;
@@ -1829,6 +1839,10 @@ extern "C" int pa_prefix_decode(const pa_plan_t* plan, int64_t prefix_len, const
       plan->q_tiles != w.q_tiles || plan->ws_bytes != w.ws_bytes(D, G, rows))
     return PA_ERR_INVALID_ARG;  // not this prefix's plan
   if (!lse_ws || !aligned16(lse_ws) || ws_bytes < plan->ws_bytes) return PA_ERR_WORKSPACE;
+  constexpr int64_t kNoWindow = int64_t(1) << 40;
+  if (!stream_fits(B, plan->n_q_heads, plan->n_kv_heads, table_stride, PS, kNoWindow, 0,
+                   prefix_len))
+    return PA_ERR_UNSUPPORTED;
   CUtensorMap tk, tv;
   PrefillArgs a;
   int st = decode_args(plan, q, k_pool, v_pool, block_table, table_stride, seq_lens, num_pages,
@@ -1885,7 +1899,7 @@ extern "C" int pa_prefix_decode(const pa_plan_t* plan, int64_t prefix_len, const
   if (e != cudaSuccess) return PA_ERR_CUDA;
 
   // Every sequence's own keys, from the prefix's end on, and the merge of all partials.
-  if (!stream_args(a, int64_t(1) << 40, 0, prefix_len)) return PA_ERR_UNSUPPORTED;
+  stream_args(a, kNoWindow, 0, prefix_len);
   a.ws_o = lse_ws + (int64_t)w.splits * rows * D;
   a.ws_lse = lse + (int64_t)w.splits * rows;
   if (w.own.stream) {

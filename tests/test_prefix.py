@@ -170,6 +170,24 @@ def test_refusals():
                                      None)) == bad
 
 
+def test_a_step_past_the_32_bit_slots_is_refused_before_anything_runs():
+    """128 sequences x 2 heads x 2^24 KV tiles of a table row: refused before the tensor maps (which
+    need a GPU's driver), and so before the prefix's kernel; 32 sequences get past it."""
+    bd = _binding()
+    lib, f = bd.load_library(), ctypes.c_void_p(1 << 20)
+    for B, want in ((128, "PA_ERR_UNSUPPORTED"), (32, "PA_ERR_CUDA")):
+        if want == "PA_ERR_CUDA" and cuda_available():
+            continue
+        pp = bd.prefix_decode_plan(16, 2, 256, 16, B, 320, 1000, "f16", num_sms=148)
+        assert bd.STATUS[lib.pa_prefix_decode(ctypes.byref(pp.plan), 320, f, f, f, f, f, 1 << 27,
+                                              f, 100, ctypes.c_void_p(1 << 30), f, 1 << 40,
+                                              None)] == want
+        wd = bd.window_decode_plan(16, 2, 256, 16, B, 1000, 2**31 - 1, 4, "f16", num_sms=148)
+        assert bd.STATUS[lib.pa_window_decode(ctypes.byref(wd.plan), 2**31 - 1, 4, f, f, f, f,
+                                              1 << 27, f, 100, ctypes.c_void_p(1 << 30), f,
+                                              1 << 40, None)] == want
+
+
 # ------------------------------------------------------------------------------------ GPU
 
 CASES = [
