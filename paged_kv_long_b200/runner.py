@@ -200,7 +200,7 @@ class ServingBatch:
     def __init__(self, n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, dtype: str,
                  batch: int, max_len: int, rope, num_pages: int, window: int = 0, n_sinks: int = 0,
                  prefix_len: int = 0, q_weight=None, k_weight=None, eps: float = 1e-6,
-                 interleaved: bool = False, device="cuda"):
+                 interleaved: bool = False, device="cuda", num_sms: int | None = None):
         import torch
         if window and prefix_len:
             raise ValueError("a shared prefix is not windowed: give one of window, prefix_len")
@@ -208,6 +208,7 @@ class ServingBatch:
             raise ValueError("prefix_len must be a multiple of the page size")
         self.shape = (n_q_heads, n_kv_heads, head_dim, page_size)
         self.dtype, self.batch, self.device = dtype, batch, torch.device(device)
+        self.num_sms = num_sms
         self.window, self.n_sinks, self.prefix_len = window, n_sinks, prefix_len
         self.rope, self.q_weight, self.k_weight = rope, q_weight, k_weight
         self.eps, self.interleaved = eps, interleaved
@@ -228,11 +229,21 @@ class ServingBatch:
         self.q_rot = None                                       # the last step's rotated queries
         args = (*self.shape, batch)
         if window:
-            self.plan = binding.window_decode_plan(*args, max_len, window, n_sinks, dtype)
+            self.plan = binding.window_decode_plan(*args, max_len, window, n_sinks, dtype,
+                                                   num_sms=num_sms)
         elif prefix_len:
-            self.plan = binding.prefix_decode_plan(*args, prefix_len, max_len, dtype)
+            self.plan = binding.prefix_decode_plan(*args, prefix_len, max_len, dtype,
+                                                   num_sms=num_sms)
         else:
-            self.plan = binding.decode_plan(*args, max_len, dtype)
+            self.plan = binding.decode_plan(*args, max_len, dtype, num_sms=num_sms)
+
+    def _check_rows(self, q, k, v, rows: int):
+        """The step's tensors hold its rows (checked before anything is cached)."""
+        Hq, Hkv, D, _ = self.shape
+        for name, t, heads in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
+            if tuple(t.shape) != (rows, heads, D) or t.dtype != self.k_pool.dtype:
+                raise ValueError(f"{name} must be {self.k_pool.dtype} of shape {(rows, heads, D)}, "
+                                 f"got {t.dtype} of {tuple(t.shape)}")
 
     def _cache(self, q, k, v, q_lens, rows: int):
         """Tables of the step, then the rotated queries; keys and values go into the pools."""
@@ -255,29 +266,37 @@ class ServingBatch:
         slots = self.prefix_table[(at // PS).long()] * PS + at % PS
         q = binding.qk_rope_append(q, k, v, at, slots, self.rope, self.k_pool, self.v_pool,
                                    self.q_weight, self.k_weight, self.eps, self.interleaved)
-        p = binding.plan(Hq, Hkv, D, PS, n, 0, self.dtype)
+        p = binding.plan(Hq, Hkv, D, PS, n, 0, self.dtype, num_sms=self.num_sms)
         return binding.prefill_combine(p, q, self.k_pool, self.v_pool, self.prefix_table)
 
     def step(self, q, k, v, q_lens):
         """Chunks of q_lens[b] rows (host lengths), packed in order; returns their attention
-        [sum q_lens, Hq, D] (fp32 without a window)."""
+        [sum q_lens, Hq, D] (fp32 without a window). A step whose chunks or attention are refused
+        has changed nothing: both are checked, and the attention planned, before its rows are
+        cached."""
         import torch
         q_lens = np.ascontiguousarray(q_lens, dtype=np.int32)
-        hist = self.hist.copy()
-        lens = torch.from_numpy(q_lens).to(self.device)
-        self._cache(q, k, v, lens, int(q_lens.sum()))
-        self.hist += q_lens
+        if q_lens.shape != (self.batch,) or (q_lens < 0).any():
+            raise ValueError("q_lens must hold a number of rows, 0 or more, for each request")
+        rows = int(q_lens.sum())
+        self._check_rows(q, k, v, rows)
         if self.window:
-            wp = binding.window_plan(*self.shape, q_lens, hist, self.window, self.n_sinks,
-                                     self.dtype)
-            return binding.window_prefill(wp, self.q_rot, self.k_pool, self.v_pool,
-                                          self.block_table)
-        bp = binding.batch_plan(*self.shape, q_lens, hist, self.dtype)
-        return binding.batch_prefill(bp, self.q_rot, self.k_pool, self.v_pool, self.block_table)
+            plan = binding.window_plan(*self.shape, q_lens, self.hist, self.window, self.n_sinks,
+                                       self.dtype, num_sms=self.num_sms)
+            attend = binding.window_prefill
+        else:
+            plan = binding.batch_plan(*self.shape, q_lens, self.hist, self.dtype,
+                                      num_sms=self.num_sms)
+            attend = binding.batch_prefill
+        lens = torch.from_numpy(q_lens).to(self.device)
+        self._cache(q, k, v, lens, rows)
+        self.hist += q_lens
+        return attend(plan, self.q_rot, self.k_pool, self.v_pool, self.block_table)
 
     def decode(self, q, k, v):
         """One token per request; returns its attention [batch, Hq, D] (fp32 without a window or
         a shared prefix). The host's lengths advance when this runs, not when a graph replays."""
+        self._check_rows(q, k, v, self.batch)
         t = self._cache(q, k, v, self.ones, self.batch)
         self.hist += 1
         pools = (self.k_pool, self.v_pool)

@@ -1,0 +1,72 @@
+"""What a ServingBatch knows and refuses on the host. On a GPU the refused steps are followed by
+accepted ones; without one the state sits on the CPU (plans are host code) and nothing is launched.
+"""
+import numpy as np
+import pytest
+
+from tests.conftest import cuda_available
+
+
+def serving(batch=2, max_len=128, num_pages=None, rope_rows=None, heads=(8, 2, 64), **kw):
+    """A ServingBatch on the CPU, and the tensors that its steps change, with their copies."""
+    import torch
+    from paged_kv_long_b200.runner import ServingBatch
+    rope = torch.zeros(rope_rows or max_len, 32)
+    pages = batch * -(-max_len // 16) if num_pages is None else num_pages
+    s = ServingBatch(*heads, 16, "f16", batch, max_len, rope, pages, device="cpu", num_sms=148,
+                     **kw)
+    state = (s.k_pool, s.v_pool, s.block_table, s.pages_used, s.hist_lens)
+    return s, state, [t.clone() for t in state]
+
+
+def rows(s, n):
+    import torch
+    Hq, Hkv, D, _ = s.shape
+    return [torch.ones(n, h, D, dtype=torch.float16) for h in (Hq, Hkv, Hkv)]
+
+
+def unchanged(s, state, before, hist):
+    import torch
+    assert all(torch.equal(a, b) for a, b in zip(state, before))
+    assert (s.hist == hist).all() and s.q_rot is None
+
+
+@pytest.fixture
+def no_launches(monkeypatch):
+    """Fails the test at the first launch of a step."""
+    from paged_kv_long_b200 import binding
+
+    def launched(*args, **kw):
+        pytest.fail("the step was under way")
+
+    for name in ("block_tables", "qk_rope_append"):
+        monkeypatch.setattr(binding, name, launched)
+
+
+@pytest.mark.parametrize("q_lens", [[3], [3, 4, 5], [-1, 4], [[3, 4]]])
+def test_chunks_that_are_not_the_batchs_change_nothing(no_launches, q_lens):
+    s, state, before = serving(window=50)
+    with pytest.raises(ValueError, match="q_lens"):
+        s.step(*rows(s, 3), q_lens)
+    unchanged(s, state, before, 0)
+
+
+def test_rows_of_another_shape_or_type_change_nothing(no_launches):
+    s, state, before = serving()
+    q, k, v = rows(s, 7)
+    for bad in ((q[:6], k, v), (q, k[:, :1], v), (q, k, v.float())):
+        with pytest.raises(ValueError):
+            s.step(*bad, [3, 4])
+    with pytest.raises(ValueError):
+        s.decode(q, k, v)  # two requests, seven rows
+    unchanged(s, state, before, 0)
+
+
+@pytest.mark.parametrize("window", [0, 50])
+def test_a_step_that_cannot_be_planned_changes_nothing(no_launches, window):
+    """600 KV heads: more row blocks than a launch's schedule holds, however few the rows."""
+    from paged_kv_long_b200 import binding
+    s, state, before = serving(heads=(600, 600, 64), window=window, max_len=16)
+    with pytest.raises(binding.PaError, match="UNSUPPORTED"):
+        s.step(*rows(s, 2), [1, 1])
+    unchanged(s, state, before, 0)
