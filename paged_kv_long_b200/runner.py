@@ -222,6 +222,8 @@ class ServingBatch:
         self.prefix_table = self.free_pages[:shared]
         self.block_table = torch.full((batch, -(-max_len // page_size)), -1, **i32)
         self.block_table[:, :shared] = self.prefix_table
+        # a request's most rows: each needs a place in its table row and a rotation
+        self.most_rows = min(self.block_table.shape[1] * page_size, rope.shape[0])
         self.pages_used = torch.full((1,), shared, **i32)
         self.hist_lens = torch.full((batch,), prefix_len, **i32)
         self.ones = torch.ones(batch, **i32)
@@ -236,6 +238,21 @@ class ServingBatch:
                                                    num_sms=num_sms)
         else:
             self.plan = binding.decode_plan(*args, max_len, dtype, num_sms=num_sms)
+
+    def check_room(self, rows):
+        """Raise ValueError unless each request b can take rows[b] more rows (one number: all of
+        them that many): none may pass its table row (max_len in whole pages) or the rotation
+        table, and the free list has to hold the pages. Past any of these the device skips a row and
+        goes on (binding.device_error tells), so ``step`` and ``decode`` ask first; the replays of a
+        captured step cannot, so ask for as many rows as there will be replays before them."""
+        shared, PS = self.prefix_table.shape[0], self.shape[3]
+        lens = self.hist + np.asarray(rows)
+        if (lens > self.most_rows).any():
+            b = int(np.argmax(lens > self.most_rows))
+            raise ValueError(f"request {b} would hold {lens[b]} rows; the most is {self.most_rows}")
+        need = int((-(-lens // PS)).sum()) - (self.batch - 1) * shared
+        if need > self.k_pool.shape[0]:
+            raise ValueError(f"the requests would hold {need} pages of {self.k_pool.shape[0]}")
 
     def _check_rows(self, q, k, v, rows: int):
         """The step's tensors hold its rows (checked before anything is cached)."""
@@ -280,6 +297,7 @@ class ServingBatch:
             raise ValueError("q_lens must hold a number of rows, 0 or more, for each request")
         rows = int(q_lens.sum())
         self._check_rows(q, k, v, rows)
+        self.check_room(q_lens)
         if self.window:
             plan = binding.window_plan(*self.shape, q_lens, self.hist, self.window, self.n_sinks,
                                        self.dtype, num_sms=self.num_sms)
@@ -297,6 +315,7 @@ class ServingBatch:
         """One token per request; returns its attention [batch, Hq, D] (fp32 without a window or
         a shared prefix). The host's lengths advance when this runs, not when a graph replays."""
         self._check_rows(q, k, v, self.batch)
+        self.check_room(1)
         t = self._cache(q, k, v, self.ones, self.batch)
         self.hist += 1
         pools = (self.k_pool, self.v_pool)
@@ -311,7 +330,8 @@ class ServingBatch:
     def capture_decode(self, q, k, v):
         """The decode step on these (static) tensors as a CUDA graph: (graph, its output). Run
         ``decode`` once before. Each replay is the next token's step: rewrite q, k and v in place,
-        replay, and count it with ``replayed`` before host lengths are needed again."""
+        replay, and count it with ``replayed`` before host lengths are needed again. Replays do not
+        ask for room (``check_room``)."""
         import torch
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):

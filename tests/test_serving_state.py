@@ -70,3 +70,41 @@ def test_a_step_that_cannot_be_planned_changes_nothing(no_launches, window):
     with pytest.raises(binding.PaError, match="UNSUPPORTED"):
         s.step(*rows(s, 2), [1, 1])
     unchanged(s, state, before, 0)
+
+
+def test_a_request_past_its_last_row_changes_nothing(no_launches):
+    """Past its table row (three pages), or past the rotation table where that is shorter; by a
+    chunk or a token."""
+    for kw, most in ((dict(max_len=40, rope_rows=99), 48), (dict(max_len=64, rope_rows=41), 41)):
+        s, state, before = serving(num_pages=50, **kw)
+        more = f"request 1 would hold {most + 1} rows; the most is {most}"
+        with pytest.raises(ValueError, match=more):
+            s.step(*rows(s, most + 4), [3, most + 1])
+        unchanged(s, state, before, 0)
+        s.hist += [7, most]  # as if replayed
+        with pytest.raises(ValueError, match=more):
+            s.decode(*rows(s, 2))
+        s.check_room([most - 7, 0])
+        with pytest.raises(ValueError, match="request 0"):
+            s.check_room([most - 6, 0])
+        unchanged(s, state, before, [7, most])
+
+
+@pytest.mark.parametrize("prefix", [0, 48])
+def test_a_step_past_the_free_pages_changes_nothing(no_launches, prefix):
+    """Seven pages past the prefix's three: whole pages of each request's own rows count."""
+    shared = prefix // 16
+    s, state, before = serving(max_len=200, num_pages=7 + shared, prefix_len=prefix)
+    unchanged(s, state, before, prefix)
+    s.check_room([16 * 6, 16])
+    for lens in ([16 * 6 + 1, 16], [16 * 7, 1], [16 * 6, 17]):
+        with pytest.raises(ValueError, match=f"{8 + shared} pages of {7 + shared}"):
+            s.step(*rows(s, sum(lens)), lens)
+    s.hist += [16 * 6, 16]
+    with pytest.raises(ValueError, match=f"{9 + shared} pages"):  # both begin a page
+        s.decode(*rows(s, 2))
+    s.hist[:] = prefix
+    s.check_room(48)
+    with pytest.raises(ValueError, match=f"{8 + shared} pages"):  # 49 replays: 4 pages each
+        s.check_room(49)
+    unchanged(s, state, before, prefix)
