@@ -298,18 +298,52 @@ class ServingBatch:
         rows = int(q_lens.sum())
         self._check_rows(q, k, v, rows)
         self.check_room(q_lens)
-        if self.window:
-            plan = binding.window_plan(*self.shape, q_lens, self.hist, self.window, self.n_sinks,
-                                       self.dtype, num_sms=self.num_sms)
-            attend = binding.window_prefill
-        else:
-            plan = binding.batch_plan(*self.shape, q_lens, self.hist, self.dtype,
-                                      num_sms=self.num_sms)
-            attend = binding.batch_prefill
+        runs = self._runs(q_lens)
         lens = torch.from_numpy(q_lens).to(self.device)
         self._cache(q, k, v, lens, rows)
         self.hist += q_lens
-        return attend(plan, self.q_rot, self.k_pool, self.v_pool, self.block_table)
+        attend = binding.window_prefill if self.window else binding.batch_prefill
+        out = torch.empty(q.shape, dtype=q.dtype if self.window else torch.float32,
+                          device=self.device)
+        for r0, r1, b0, b1, plan in runs:
+            attend(plan, self.q_rot[r0:r1], self.k_pool, self.v_pool, self.block_table[b0:b1],
+                   out[r0:r1])
+        return out
+
+    def _runs(self, q_lens):
+        """The attention launches of a step: (packed rows r0 .. r1, requests b0 .. b1, their plan).
+        One, unless the planner has no room for so many row blocks or requests: then the rows are
+        halved until it has (every key is cached before any row attends, so a chunk may be cut)."""
+        def planned(lens, hist):
+            if self.window:
+                return binding.window_plan(*self.shape, lens, hist, self.window, self.n_sinks,
+                                           self.dtype, num_sms=self.num_sms)
+            return binding.batch_plan(*self.shape, lens, hist, self.dtype, num_sms=self.num_sms)
+
+        edge = np.concatenate([[0], np.cumsum(q_lens, dtype=np.int64)])
+
+        def cut(r0, r1):
+            b0 = int(np.searchsorted(edge, r0, "right")) - 1  # the requests with rows in between
+            b1 = int(np.searchsorted(edge, r1, "left"))
+            at = np.clip(edge[b0:b1 + 1], r0, r1)
+            try:
+                return [(r0, r1, b0, b1,
+                         planned(np.diff(at), self.hist[b0:b1] + at[:-1] - edge[b0:b1]))]
+            except binding.PaError as e:
+                if binding.STATUS[e.status] != "PA_ERR_UNSUPPORTED" or r1 - r0 < 2:
+                    raise
+            mid = (r0 + r1) // 2
+            return cut(r0, mid) + cut(mid, r1)
+
+        rows = int(edge[-1])
+        if rows == 0:
+            return []
+        try:
+            return [(0, rows, 0, self.batch, planned(q_lens, self.hist))]
+        except binding.PaError as e:
+            if binding.STATUS[e.status] != "PA_ERR_UNSUPPORTED":
+                raise
+        return cut(0, rows)
 
     def decode(self, q, k, v):
         """One token per request; returns its attention [batch, Hq, D] (fp32 without a window or

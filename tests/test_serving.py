@@ -182,3 +182,59 @@ def test_gpu_two_servers_share_the_device():
     for r in range(2):
         a.check_attention(r, (40, 50)[r] + 2, a.s.q_rot[r], outs[0][r], window=30, sinks=2)
         b.check_attention(r, (40, 50)[r] + 2, b.s.q_rot[r], outs[1][r], window=64)
+
+
+@pytest.mark.parametrize("window", [0, 40])
+def test_gpu_step_of_more_requests_than_a_launch_holds(window):
+    attn = dict(window=window, sinks=2) if window else {}
+    kw = dict(window=window, n_sinks=2) if window else {}
+    run(Server(6, 300, 64, **kw), [[1] * 300, [0, 3] * 150], 1, 0, **attn)
+
+
+@pytest.mark.parametrize("window", [0, 1000])
+def test_gpu_chunk_of_more_rows_than_a_launch_holds(window):
+    """16,600 rows of one request: more than 512 row blocks. Rows on both sides of each cut, and a
+    step without any row."""
+    import torch
+    from paged_kv_long_b200 import binding
+    attn = dict(window=window, sinks=2) if window else {}
+    srv = Server(7, 2, 16700, "bf16", **(dict(window=window, n_sinks=2) if window else {}))
+    binding.device_error(reset=True)
+    q, k, v = srv.feed([20, 9])
+    srv.s.step(q.cuda(), k.cuda(), v.cuda(), [20, 9])
+    lens = [16600, 77]
+    edges = [r[1] for r in srv.s._runs(np.array(lens, np.int32))]
+    assert len(edges) > 1
+    q, k, v = srv.feed(lens)
+    out = srv.s.step(q.cuda(), k.cuda(), v.cuda(), lens)
+    none = [x[:0].cuda() for x in (q, k, v)]
+    q_rot = srv.s.q_rot
+    assert srv.s.step(*none, [0, 0]).shape == (0, HQ, D)
+    torch.cuda.synchronize()
+    assert binding.device_error(reset=True)[0] == 0
+    for row in {0, 16599, 16600, 16676}.union(*({e - 1, e} for e in edges[:-1])):
+        b, pos = (0, 20 + row) if row < 16600 else (1, 9 + row - 16600)
+        srv.check_attention(b, pos, q_rot[row], out[row], **attn)
+
+
+def test_gpu_refused_steps_then_accepted_ones():
+    """Steps without room change nothing: what follows is as if they had not been asked for."""
+    import torch
+    srv = Server(8, 3, 96, window=50, n_sinks=4)
+    state = lambda: [t.clone() for t in (srv.s.k_pool, srv.s.v_pool,  # noqa: E731
+                                         srv.s.block_table, srv.s.pages_used, srv.s.hist_lens)]
+    before = state()
+    q, k, v = (x.cuda() for x in srv.rows(3 + 97))
+    with pytest.raises(ValueError, match="request 1 would hold 97"):
+        srv.s.step(q, k, v, [3, 97, 0])
+    assert all(torch.equal(a, b) for a, b in zip(state(), before))
+    run(srv, [[3, 90, 0], [5, 4, 96]], 0, 0, window=50, sinks=4)
+    with pytest.raises(ValueError, match="request 2"):
+        srv.s.decode(q[:3], k[:3], v[:3])
+    run_on = [[2, 2, 0]]  # up to the last rows of request 1
+    pos = srv.s.hist.copy()
+    q, k, v = srv.feed(run_on[0])
+    out = srv.s.step(q.cuda(), k.cuda(), v.cuda(), run_on[0])
+    torch.cuda.synchronize()
+    for b, row in ((0, 1), (1, 3)):
+        srv.check_attention(b, pos[b] + 1, srv.s.q_rot[row], out[row], window=50, sinks=4)

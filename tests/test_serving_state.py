@@ -108,3 +108,39 @@ def test_a_step_past_the_free_pages_changes_nothing(no_launches, prefix):
     with pytest.raises(ValueError, match=f"{8 + shared} pages"):  # 49 replays: 4 pages each
         s.check_room(49)
     unchanged(s, state, before, prefix)
+
+
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("seed", range(6))
+def test_launches_of_a_step_cover_its_rows(window, seed):
+    """Too many requests, or rows, for one launch: the launches' chunks laid end to end are the
+    step's, each behind the keys that come before it; a step that fits is one launch."""
+    rng = np.random.default_rng(seed)
+    batch = int(rng.choice([1, 3, 257, 600]))
+    s, _, _ = serving(batch=batch, max_len=40000, num_pages=4, window=window, heads=(8, 4, 64))
+    s.hist += rng.integers(0, 300, batch)
+    lens = rng.integers(0, 2, batch) * rng.integers(0, 60, batch)
+    if seed % 2 or batch < 4:
+        lens[rng.integers(0, batch)] = 30000
+    runs = s._runs(lens.astype(np.int32))
+    if max(lens) == 30000 or np.ptp(np.flatnonzero(lens)) >= 256:
+        assert len(runs) > 1
+    at, done, end = 0, np.zeros(batch, int), 0
+    for r0, r1, b0, b1, plan in runs:
+        assert r0 == end and r1 > r0
+        q, h = plan.q_lens, plan.hist_lens
+        assert len(q) == len(h) == b1 - b0 and q.sum() == r1 - r0
+        some = q > 0  # (no row, no history that counts)
+        assert (h[some] == (s.hist + done)[b0:b1][some]).all()
+        # packed order: every request before the run's first is done, the last may go on
+        assert (done[:b0] == lens[:b0]).all() and (done[b0 + 1:] == 0).all()
+        done[b0:b1] += q
+        end = r1
+    assert (done == lens).all() and end == lens.sum()
+    small = np.zeros(batch, np.int32)
+    small[:100:7] = 3
+    fits = s._runs(small)
+    assert sum(r[1] - r[0] for r in fits) == small.sum()
+    if batch < 257:
+        assert [r[:4] for r in fits] == [(0, small.sum(), 0, batch)]
+    assert s._runs(np.zeros(batch, np.int32)) == []
