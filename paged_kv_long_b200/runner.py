@@ -195,6 +195,9 @@ class ServingBatch:
     length on the device, so that ``capture_decode`` can record it once as a CUDA graph and each
     replay is the next token's step. A shared prefix is written first (``write_prefix``); every
     request then begins after it. Pages are taken from the free list in order and not given back.
+
+    The constructor waits for its own work (and what its stream held before), so the first step may
+    run on any stream; steps on different streams are the caller's to order.
     """
 
     def __init__(self, n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, dtype: str,
@@ -238,6 +241,8 @@ class ServingBatch:
                                                    num_sms=num_sms)
         else:
             self.plan = binding.decode_plan(*args, max_len, dtype, num_sms=num_sms)
+        if self.device.type == "cuda":
+            torch.cuda.current_stream(self.device).synchronize()
 
     def check_room(self, rows):
         """Raise ValueError unless each request b can take rows[b] more rows (one number: all of

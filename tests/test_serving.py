@@ -238,3 +238,19 @@ def test_gpu_refused_steps_then_accepted_ones():
     torch.cuda.synchronize()
     for b, row in ((0, 1), (1, 3)):
         srv.check_attention(b, pos[b] + 1, srv.s.q_rot[row], out[row], window=50, sinks=4)
+
+
+def test_gpu_constructor_leaves_nothing_pending():
+    """Steps on a fresh stream right after the constructor need no wait: its fills are done, and so
+    is the work that its tensors may come from."""
+    import torch
+    torch.cuda._sleep(20_000_000)  # about 10 ms of the constructor's stream
+    srv = Server(9, 2, 200, window=64)
+    assert torch.cuda.current_stream().query()
+    s = torch.cuda.Stream()
+    fed = srv.feed([40, 50])
+    with torch.cuda.stream(s):
+        out = srv.s.step(*(x.cuda() for x in fed), [40, 50])
+    s.synchronize()
+    for b, row in ((0, 39), (1, 89)):
+        srv.check_attention(b, (39, 49)[b], srv.s.q_rot[row], out[row], window=64)
