@@ -529,9 +529,11 @@ class WindowPlan(_StepPlan):
             self.lens_ptrs = (q_lens.ctypes.data, hist_lens.ctypes.data)
 
 
-def _num_sms() -> int:
+def _num_sms(device=None) -> int:
+    """SMs of a device, the current one if none is given."""
     import torch
-    return torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    return torch.cuda.get_device_properties(torch.cuda.current_device() if device is None
+                                            else device).multi_processor_count
 
 
 def _window_args(window, n_sinks):

@@ -211,6 +211,8 @@ class ServingBatch:
             raise ValueError("prefix_len must be a multiple of the page size")
         self.shape = (n_q_heads, n_kv_heads, head_dim, page_size)
         self.dtype, self.batch, self.device = dtype, batch, torch.device(device)
+        if self.device.type == "cuda" and num_sms is None:
+            num_sms = binding._num_sms(self.device)
         self.num_sms = num_sms
         self.window, self.n_sinks, self.prefix_len = window, n_sinks, prefix_len
         self.rope, self.q_weight, self.k_weight = rope, q_weight, k_weight
@@ -372,9 +374,10 @@ class ServingBatch:
         replay, and count it with ``replayed`` before host lengths are needed again. Replays do not
         ask for room (``check_room``)."""
         import torch
-        graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(graph):
-            out = self.decode(q, k, v)
+        with torch.cuda.device(self.device):  # a capture is of the current device's stream
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                out = self.decode(q, k, v)
         self.hist -= 1  # captured, not run
         return graph, out
 

@@ -144,3 +144,33 @@ def test_launches_of_a_step_cover_its_rows(window, seed):
     if batch < 257:
         assert [r[:4] for r in fits] == [(0, small.sum(), 0, batch)]
     assert s._runs(np.zeros(batch, np.int32)) == []
+
+
+def test_plans_and_captures_are_the_own_devices(monkeypatch):
+    """A batch on device 1 while device 0 is current: plans for device 1's SMs, and a capture that
+    device 1's stream is in (the calls themselves go by their tensors)."""
+    import contextlib
+    import types
+    import torch
+    from paged_kv_long_b200 import binding
+    sms = {0: 100, 1: 37}
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "get_device_properties", lambda d: types.SimpleNamespace(
+        multi_processor_count=sms[d if isinstance(d, int) else d.index]))
+    assert binding._num_sms() == 100 and binding._num_sms(torch.device("cuda", 1)) == 37
+    s, _, _ = serving()
+    s.device, inside = torch.device("cuda", 1), []
+
+    @contextlib.contextmanager
+    def switched(device):
+        inside.append(device)
+        yield
+        inside.pop()
+
+    seen = []
+    monkeypatch.setattr(torch.cuda, "device", switched)
+    monkeypatch.setattr(torch.cuda, "CUDAGraph", lambda: seen.append(("graph", *inside)))
+    monkeypatch.setattr(torch.cuda, "graph", lambda g: switched("capture"))
+    monkeypatch.setattr(s, "decode", lambda q, k, v: seen.append(("decode", *inside)))
+    s.capture_decode(None, None, None)
+    assert seen == [("graph", s.device), ("decode", s.device, "capture")] and not inside
