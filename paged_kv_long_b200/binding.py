@@ -423,8 +423,8 @@ class BatchPlan:
     def __init__(self, plan: Plan, q_lens, hist_lens):
         import numpy as np
         self.plan = plan
-        self.q_lens = np.ascontiguousarray(q_lens, dtype=np.int32)
-        self.hist_lens = np.ascontiguousarray(hist_lens, dtype=np.int64)
+        self.q_lens = np.array(q_lens, dtype=np.int32)  # copies: the plan's own
+        self.hist_lens = np.array(hist_lens, dtype=np.int64)
 
     def _arrays(self):
         return self.q_lens.ctypes.data, self.hist_lens.ctypes.data

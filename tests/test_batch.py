@@ -372,3 +372,13 @@ def test_one_row_batches_plan_two_cta_slots_per_sm():
     for Hq, D, q_lens in ((32, 256, ones), (16, 64, ones), (16, 256, 2 * ones)):
         bp = bd.batch_plan(Hq, 2, D, 16, q_lens, hist, "bf16", num_sms=148)
         assert bp.plan.units < 2 * 148
+
+
+def test_batch_plan_keeps_its_own_lengths():
+    """Arrays that the caller changes afterwards (its lengths advance) are not the plan's."""
+    from paged_kv_long_b200 import binding as bd
+    rows, hist = np.array([3, 5], np.int32), np.array([9, 0], np.int64)
+    bp = bd.batch_plan(4, 2, 64, 16, rows, hist, num_sms=148)
+    rows += 100
+    hist += 100
+    assert bp.q_lens.tolist() == [3, 5] and bp.hist_lens.tolist() == [9, 0]
