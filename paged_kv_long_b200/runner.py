@@ -224,11 +224,14 @@ class ServingBatch:
         self.v_pool = torch.zeros(pool, dtype=dt, device=self.device)
         self.free_pages = torch.arange(num_pages, **i32)
         shared = prefix_len // page_size
-        self.prefix_table = self.free_pages[:shared]
         self.block_table = torch.full((batch, -(-max_len // page_size)), -1, **i32)
-        self.block_table[:, :shared] = self.prefix_table
         # a request's most rows: each needs a place in its table row and a rotation
         self.most_rows = min(self.block_table.shape[1] * page_size, rope.shape[0])
+        if not 0 <= prefix_len <= self.most_rows or shared > num_pages:
+            raise ValueError(f"a prefix of {prefix_len} rows: a request holds {self.most_rows} at "
+                             f"most, and there are {num_pages} pages of {page_size}")
+        self.prefix_table = self.free_pages[:shared]
+        self.block_table[:, :shared] = self.prefix_table
         self.pages_used = torch.full((1,), shared, **i32)
         self.hist_lens = torch.full((batch,), prefix_len, **i32)
         self.ones = torch.ones(batch, **i32)

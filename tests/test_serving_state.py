@@ -174,3 +174,12 @@ def test_plans_and_captures_are_the_own_devices(monkeypatch):
     monkeypatch.setattr(s, "decode", lambda q, k, v: seen.append(("decode", *inside)))
     s.capture_decode(None, None, None)
     assert seen == [("graph", s.device), ("decode", s.device, "capture")] and not inside
+
+
+def test_a_prefix_without_room_is_refused():
+    """Past the table row, the pages, or the rotation table (whose rows the device would skip)."""
+    for kw in (dict(max_len=40, rope_rows=99, prefix_len=64), dict(prefix_len=64, num_pages=3),
+               dict(prefix_len=64, rope_rows=63), dict(prefix_len=-16)):
+        with pytest.raises(ValueError, match="a prefix of"):
+            serving(**kw)
+    assert serving(prefix_len=64, rope_rows=64, num_pages=4)[0].most_rows == 64
