@@ -297,7 +297,8 @@ int pa_batch_combine(const pa_plan_t* plan, const int32_t* q_lens, const int64_t
  *   out has the type of q: the sums are fp32, split partials too, and the row is rounded once. It
  * may not overlap q. Calls that may overlap on the GPU (other streams, other captured graphs)
  * need workspaces of their own.
- * Softmax and products are those of pa_prefill (probabilities rounded to the input type).
+ * Softmax and products are those of pa_prefill (probabilities rounded to the input type, which
+ * the tensor cores need; their sum, and all other arithmetic, is fp32).
  * The pages have no counterpart; it is the attention of models whose local layers see a window,
  * and of caches bounded to a window and the first tokens.
  *
@@ -359,7 +360,8 @@ int pa_window_decode(const pa_plan_t* plan, int window, int n_sinks, const void*
  *                 entries of the first prefix_len / PS pages are not read.
  *   seq_lens      device int32 [batch]: keys of each whole sequence. A sequence of at most
  *                 prefix_len keys sees its first seq_lens[b] shared ones; one with no key (a
- *                 padded row) gets zeros.
+ *                 padded row) gets zeros. (A non-finite shared key or value may reach a sequence
+ *                 that ends before it: the sequences share the prefix's tiles.)
  *   out           device [batch][Hq][D] of dtype; it may not overlap q.
  *   lse_ws        workspace of plan->ws_bytes. The call merges its partials itself.
  * The plan's policy is PA_POLICY_PREFIX_DECODE, splits the prefix's splits, units those of the own

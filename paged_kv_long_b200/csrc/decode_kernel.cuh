@@ -20,7 +20,8 @@
 // also carries a failed wait to every warp so that all leave the loop together); the running
 // maximum is the same in every thread, the sums of the weights are per thread and added up
 // once at the end. O^T is rescaled (a column per head, by the threads that own its lanes)
-// only when some head's maximum grows by more than 2^8, as in the prefill kernels.
+// only when some head's maximum grows by more than 2^8, as in the prefill kernels. P is rounded to
+// the input type as there, the sums are of unrounded weights.
 
 constexpr int kDecN = 16;                // N of both MMAs (heads 8..15 repeat 0..7)
 constexpr int kDecSlots = 6;             // ring slots per CTA

@@ -16,7 +16,9 @@
 // Each CTA finds its run by itself: a block scan of the units' slots over runs of sequences (one
 // each up to 256), then a walk. A segment that is a whole unit writes its output rows; a part of
 // a unit leaves its rows and base-2 LSE in the CTA's workspace slot 0 (the CTA's first segment)
-// or 1 (its last), which merge_stream_kernel joins after the same scan.
+// or 1 (its last), which merge_stream_kernel joins after the same scan. Roundings: P to the input
+// type (see prefill_kernel) and a whole unit's or merged row's output; partials, their LSEs and all
+// sums are fp32.
 
 constexpr int kStreamRuns = 256;  // runs of sequences in the scan (= threads of both kernels)
 static_assert(kStreamRuns == kThreads, "one run a thread");

@@ -80,8 +80,9 @@ DecodeWork decode_work(int num_sms, int D, int G, int Hkv, int64_t batch, int64_
 
 // A decode step over a shared prefix: the prefix's packed (sequence, head) rows in `q_tiles` tiles
 // a KV head, on `per` CTAs a unit, `splits` uniform splits of its keys; the sequences' own keys as
-// decode_work shares them, on `own.units` CTAs beside the prefix's where that is the shorter. Workspace rows: the prefix's partials [splits][rows], then the own
-// part's: [rows] of whole units and the part slots (stream kernel), or its uniform partials.
+// decode_work shares them, on `own.units` CTAs beside the prefix's where that is the shorter.
+// Workspace rows: the prefix's partials [splits][rows], then the own part's: [rows] of whole units
+// and the part slots (stream kernel), or its uniform partials.
 struct PrefixWork {
   int32_t per, q_tiles, splits;
   DecodeWork own;

@@ -13,7 +13,8 @@
 // columns) goes over the lower half of its S: a thread works through its row in chunks of 32
 // scores, and chunk k's 16 columns of P end below the scores not yet read. A row's maximum is
 // taken in a first pass over S, the exponentials in a second, so a thread holds 64 scores at a
-// time and 384 threads fit (168 registers each).
+// time and 384 threads fit (168 registers each; ptxas spills 84-88 bytes of them). P is rounded to
+// the input type (see prefill_kernel).
 //
 // Each issuing warp runs PV(j), QK(j+1) of its tile: while one group's softmax works, the other
 // tile's two products do. A thread that issues for both tiles loses ~950 cycles a tile to its

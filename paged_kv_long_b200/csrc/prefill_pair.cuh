@@ -241,7 +241,8 @@ __device__ __forceinline__ void softmax_pair_role(const PrefillArgs& a, const So
       ok = false;
       break;
     }
-    // P(j) (rounded to the input type) into P buffer j % 2: one row per lane, 16-bit pairs
+    // P(j) (rounded to the input type, see prefill_kernel) into P buffer j % 2: one row per lane,
+    // 16-bit pairs
     const uint32_t p_col = kPairPCol + 64u * (uint32_t)(j & 1);
     tmem_st32u(t_lane + p_col, *reinterpret_cast<const uint32_t(*)[32]>(&pk[0]));
     tmem_st32u(t_lane + p_col + 32u, *reinterpret_cast<const uint32_t(*)[32]>(&pk[32]));
