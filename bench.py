@@ -37,9 +37,9 @@ L2_FLUSH_BYTES = 512 << 20
 # sources hash to `sources`; after any change to them the bench reports null until the
 # captures are taken again.
 TRAFFIC_CAPTURE = {
-    "workload": "c5", "sources": "f3a03425df03feea", "bytes_per_launch": 112.82e6,
+    "workload": "c5", "sources": "150e3b506f353a22", "bytes_per_launch": 110.46e6,
     "how": ("ncu dram__bytes_read.sum + dram__bytes_write.sum of one launch each of chunks 0, 3, "
-            "6, 9, 12 and 15 (21.1, 39.6, 64.6, 93.8, 153.7, 353.8 MB; three launches per capture "
+            "6, 9, 12 and 15 (21.1, 41.2, 65.3, 93.7, 152.2, 334.0 MB; three launches per capture "
             "of bench.py --section piece), linear in between, mean over the 16 chunks")}
 
 

@@ -643,3 +643,44 @@ def test_gpu_nan_reaches_the_output(Hq, Hkv, D, L):
         assert torch.equal(got[~rows], want[~rows]), name
         assert bool(keys[1].isnan().all()), name
         assert torch.equal(keys[[0, 2]], want[[0, 2]]), name
+
+
+@_gpu
+@pytest.mark.parametrize("Hq,Hkv,D,PS", [(16, 2, 256, 64), (8, 4, 64, 16)])
+def test_gpu_pages_past_2_to_31_elements(Hq, Hkv, D, PS):
+    """Pages whose elements lie past 2^31 (their bytes past 2^32) of a pool: attention and the cache
+    write give the bits that the same pages give in a small one, and write nowhere else."""
+    import torch
+    bd = _binding()
+    bd.device_error(reset=True)
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda").half()  # noqa: E731
+    B, L, prefix = 4, 1500, 1024
+    n, common = -(-L // PS), prefix // PS
+    pages = common + B * (n - common)
+    far = 2**31 // (PS * Hkv * D) + 1  # the first of the far pages
+    small = [rand(pages, PS, Hkv, D) for _ in range(2)]
+    large = [torch.zeros(far + pages, PS, Hkv, D, dtype=torch.half, device="cuda")
+             for _ in range(2)]
+    for x, y in zip(large, small):
+        x[far:] = y
+    table = torch.arange(n, device="cuda", dtype=torch.int32).repeat(B, 1)
+    table[:, common:] += (n - common) * torch.arange(B, device="cuda", dtype=torch.int32)[:, None]
+    lens = torch.tensor([L, 1300, prefix, 77], dtype=torch.int32, device="cuda")
+    q, rows = rand(B, Hq, D), rand(231, Hq, D)
+    wd = bd.window_decode_plan(Hq, Hkv, D, PS, B, L, 700, 20, "f16")
+    wp = bd.window_plan(Hq, Hkv, D, PS, [1, 200, 30, 0], [L - 1, 1000, 900, 5], 700, 20, "f16")
+    pd = bd.prefix_decode_plan(Hq, Hkv, D, PS, B, prefix, L, "f16")
+    for run in (lambda k, v, t: bd.window_decode(wd, q, k, v, t, lens),
+                lambda k, v, t: bd.window_prefill(wp, rows, k, v, t),
+                lambda k, v, t: bd.prefix_decode(pd, q, k, v, t[0, :common].clone(), t, lens)):
+        assert torch.equal(run(*small, table), run(*large, table + far))
+    T = 100
+    x = [rand(T, h, D) for h in (Hq, Hkv, Hkv)]
+    slots = torch.randperm(pages * PS, generator=gen, device="cuda")[:T].int()
+    pos, rope = torch.arange(T, dtype=torch.int32, device="cuda"), bd.rope_table(T, D)
+    a = bd.qk_rope_append(*x, pos, slots, rope, *small)
+    b = bd.qk_rope_append(*x, pos, slots + far * PS, rope, *large)
+    assert torch.equal(a, b) and bd.device_error(reset=True)[0] == 0
+    for x, y in zip(large, small):
+        assert torch.equal(x[far:], y) and not x[:far].any()
