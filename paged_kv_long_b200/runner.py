@@ -210,7 +210,8 @@ class ServingBatch:
         if prefix_len % page_size:
             raise ValueError("prefix_len must be a multiple of the page size")
         self.shape = (n_q_heads, n_kv_heads, head_dim, page_size)
-        self.dtype, self.batch, self.device = dtype, batch, torch.device(device)
+        self.dtype, self.batch = dtype, batch
+        self.device = torch.empty(0, device=device).device  # "cuda": the one that is current now
         if self.device.type == "cuda" and num_sms is None:
             num_sms = binding._num_sms(self.device)
         self.num_sms = num_sms
@@ -268,9 +269,10 @@ class ServingBatch:
         """The step's tensors hold its rows (checked before anything is cached)."""
         Hq, Hkv, D, _ = self.shape
         for name, t, heads in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
-            if tuple(t.shape) != (rows, heads, D) or t.dtype != self.k_pool.dtype:
-                raise ValueError(f"{name} must be {self.k_pool.dtype} of shape {(rows, heads, D)}, "
-                                 f"got {t.dtype} of {tuple(t.shape)}")
+            want = ((rows, heads, D), self.k_pool.dtype, self.device)
+            if (tuple(t.shape), t.dtype, t.device) != want:
+                raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}, {t.dtype}, "
+                                 f"{t.device}")
 
     def _cache(self, q, k, v, q_lens, rows: int):
         """Tables of the step, then the rotated queries; keys and values go into the pools."""

@@ -254,3 +254,10 @@ def test_gpu_constructor_leaves_nothing_pending():
     s.synchronize()
     for b, row in ((0, 39), (1, 89)):
         srv.check_attention(b, (39, 49)[b], srv.s.q_rot[row], out[row], window=64)
+
+
+def test_gpu_device_is_the_one_of_the_constructor():
+    """Given without a number: the device that is current then, whatever is current at a step."""
+    import torch
+    srv = Server(10, 2, 64)
+    assert srv.s.device == srv.s.k_pool.device == torch.device("cuda", torch.cuda.current_device())

@@ -51,10 +51,10 @@ def test_chunks_that_are_not_the_batchs_change_nothing(no_launches, q_lens):
     unchanged(s, state, before, 0)
 
 
-def test_rows_of_another_shape_or_type_change_nothing(no_launches):
+def test_rows_of_another_shape_type_or_device_change_nothing(no_launches):
     s, state, before = serving()
     q, k, v = rows(s, 7)
-    for bad in ((q[:6], k, v), (q, k[:, :1], v), (q, k, v.float())):
+    for bad in ((q[:6], k, v), (q, k[:, :1], v), (q, k, v.float()), (q, k.to("meta"), v)):
         with pytest.raises(ValueError):
             s.step(*bad, [3, 4])
     with pytest.raises(ValueError):
