@@ -304,12 +304,13 @@ class ServingBatch:
         has changed nothing: both are checked, and the attention planned, before its rows are
         cached."""
         import torch
-        q_lens = np.ascontiguousarray(q_lens, dtype=np.int32)
+        q_lens = np.asarray(q_lens, dtype=np.int64)
         if q_lens.shape != (self.batch,) or (q_lens < 0).any():
             raise ValueError("q_lens must hold a number of rows, 0 or more, for each request")
         rows = int(q_lens.sum())
         self._check_rows(q, k, v, rows)
         self.check_room(q_lens)
+        q_lens = q_lens.astype(np.int32)  # below 2^31: there is room for them
         runs = self._runs(q_lens)
         lens = torch.from_numpy(q_lens).to(self.device)
         self._cache(q, k, v, lens, rows)

@@ -183,3 +183,11 @@ def test_a_prefix_without_room_is_refused():
         with pytest.raises(ValueError, match="a prefix of"):
             serving(**kw)
     assert serving(prefix_len=64, rope_rows=64, num_pages=4)[0].most_rows == 64
+
+
+def test_lengths_past_32_bits_are_not_folded(no_launches):
+    """2^32 + 3 rows are not 3."""
+    s, state, before = serving()
+    with pytest.raises(ValueError):
+        s.step(*rows(s, 7), np.array([2**32 + 3, 4]))
+    unchanged(s, state, before, 0)
